@@ -39,7 +39,8 @@ constexpr size_t kErrBytes = 256;
 enum KernelId {
   KID_REFPACK = 0, KID_CAND_SIMT, KID_CAND_TC, KID_ENCODE_SIMT, KID_ENCODE_TC, KID_RECONSTRUCT, KID_DEC_REF,
   KID_DEC_PREP, KID_DEC_STREAM_SIMT, KID_DEC_STREAM_TC, KID_DEC_COMBINE, KID_DEC_FINAL,
-  KID_APPEND_REFS, KID_APPEND_ROWS, KID_SPARSE_ATTEND, KID_SPARSE_MERGE, KID_SPARSE_SELECT, KID_COUNT
+  KID_APPEND_REFS, KID_APPEND_ROWS, KID_SPARSE_ATTEND, KID_SPARSE_MERGE, KID_SPARSE_SELECT,
+  KID_KV_APPEND, KID_KV_ATTEND, KID_KV_JOIN, KID_KV_SELECT, KID_KV_MOVE, KID_COUNT
 };
 const char* kernel_name(int id);
 
@@ -207,6 +208,63 @@ cudaError_t launch_decode_sparse_tc(const Plan& p, int T, const void* q, int64_t
 cudaError_t launch_decode(const Plan& p, const CacheView& cv, const SeqLens& sl, const void* q, int64_t qsb,
                           int64_t qsh, const void* W3, const float* b3, const void* W4, const float* b4, float* out,
                           int64_t osb, int64_t osh, void* ws, cudaStream_t st);
+
+// ---- plain paged cache ----
+// Kernel-side view of a deltakv_kv_cache: row r of pair bh (sequence-major
+// (sequence, kv-head)) is row r & (page - 1) of page ptab[bh * max_pages + (r
+// >> page_log)].
+struct KvView {
+  char* k;
+  char* v;
+  const int32_t* ptab;
+  const int32_t* lens;
+  int32_t n_pages, page_log, max_pages, max_len;
+  uint32_t* err;
+#ifdef __CUDACC__
+  __device__ void report(uint32_t detail) const {
+    if (atomicCAS(err, 0u, (uint32_t)DELTAKV_ERR_DEVICE_BOUNDS) == 0u) err[1] = detail;
+  }
+  // valid rows of a pair; a length out of range is none
+  __device__ int len(int64_t bh) const {
+    const int n = lens[bh];
+    return n < 0 || n > max_len ? 0 : n;
+  }
+  // pool row of row r of pair bh, or -1 where its page is out of range
+  __device__ int64_t row(int64_t bh, int r) const {
+    const int32_t pg = ptab[bh * max_pages + (r >> page_log)];
+    if (pg < 0 || pg >= n_pages) {
+      report((uint32_t)pg);
+      return -1;
+    }
+    return ((int64_t)pg << page_log) + (r & ((1 << page_log) - 1));
+  }
+#endif
+};
+
+// Workspace regions of the kv calls (bytes from the base; each after the
+// error word).
+constexpr int kKvMaxGrid = 2 * kNumSMs;  // CTAs of the attention's split
+// floats of one partial result (a multiple of 16 bytes)
+__host__ __device__ constexpr int kv_part_floats(int G, int d_h) { return G * d_h + 2 * kMaxG; }
+struct KvWorkspace {
+  size_t part;    // attention: [kKvMaxGrid][2] partial results of kv_part_floats
+  size_t lse2;    // attention: [B H][G] float32 log-sum-exp in units of log2 of the pairs one CTA holds whole
+  size_t logits;  // attention with weights: [B H][max_len][G] float32, in units of log2
+  size_t attend_end, weights_end;
+  size_t count, hole, move;  // eviction: [B H] moves, their target and source rows [B H][max_len / 2]
+  size_t evict_end;
+};
+KvWorkspace kv_workspace(const Plan& p, int max_len);
+
+cudaError_t launch_kv_append(const Plan& p, const KvView& c, int n_new, const KVView& kv, const int32_t* n_tokens,
+                             const int32_t* first_pos, float* w, int32_t* pos, int cap, const float* tok_w,
+                             cudaStream_t st);
+cudaError_t launch_kv_attend(const Plan& p, const KvView& c, const void* q, int64_t qsb, int64_t qsh, float* out,
+                             int64_t osb, int64_t osh, float* lse, float* w, int cap, float decay, void* ws,
+                             cudaStream_t st);
+cudaError_t launch_kv_evict(const Plan& p, const KvView& c, const int32_t* budget, int n_first, int n_recent,
+                            const float* w, const int32_t* pos, float* w_out, int32_t* pos_out, int cap,
+                            int32_t* lens_out, void* ws, cudaStream_t st);
 
 }  // namespace dkv
 

@@ -30,7 +30,8 @@ SYMBOLS = ("deltakv_plan", "deltakv_plan_destroy", "deltakv_get_cache_layout", "
            "deltakv_decode_attention_noalloc", "deltakv_reconstruct", "deltakv_device_status",
            "deltakv_set_profiling", "deltakv_profile_collect", "deltakv_status_string", "deltakv_version",
            "deltakv_test_activation", "deltakv_page_pool_layout", "deltakv_pages_from_cache",
-           "deltakv_decode_attention_paged")
+           "deltakv_decode_attention_paged", "deltakv_kv_pool_layout", "deltakv_kv_append",
+           "deltakv_kv_decode_attention", "deltakv_kv_evict")
 
 # forms of deltakv_test_activation (include/deltakv_testing.h)
 TEST_ACT_GELU_ERFF, TEST_ACT_GELU_FAST, TEST_ACT_GELU_FAST2, TEST_ACT_GELU_TANH, TEST_ACT_GELU_TANHFIT2 = 0, 1, 2, 3, 4
@@ -61,6 +62,17 @@ class _PageLayout(ctypes.Structure):
                 ("ref_k_offset", ctypes.c_size_t), ("ref_v_offset", ctypes.c_size_t),
                 ("code_offset", ctypes.c_size_t), ("idx_offset", ctypes.c_size_t),
                 ("code_scale_offset", ctypes.c_size_t), ("pool_bytes", ctypes.c_size_t)]
+
+
+class _KvLayout(ctypes.Structure):
+    _fields_ = [("k_offset", ctypes.c_size_t), ("v_offset", ctypes.c_size_t), ("pool_bytes", ctypes.c_size_t),
+                ("workspace_bytes", ctypes.c_size_t), ("weights_workspace_bytes", ctypes.c_size_t)]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("pool", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("tokens_per_page", ctypes.c_int32),
+                ("page_table", ctypes.c_void_p), ("max_pages", ctypes.c_int32), ("lens", ctypes.c_void_p),
+                ("max_len", ctypes.c_int32)]
 
 
 class _KernelTime(ctypes.Structure):
@@ -117,6 +129,15 @@ def load_library(path: str = LIB_PATH):
     lib.deltakv_decode_attention_paged.argtypes = [vp, vp, i32, vp, i64p, vp, i32, vp, i32, vp, vp, vp, vp, vp,
                                                    i64p, vp, sz, vp]
     lib.deltakv_decode_attention_paged.restype = ctypes.c_int
+    f32, kvc = ctypes.c_float, ctypes.POINTER(_KvCache)
+    lib.deltakv_kv_pool_layout.argtypes = [vp, i32, i32, i32, ctypes.POINTER(_KvLayout)]
+    lib.deltakv_kv_pool_layout.restype = ctypes.c_int
+    lib.deltakv_kv_append.argtypes = [vp, kvc, i32, vp, vp, i64p, vp, vp, vp, vp, i32, vp, vp, sz, vp]
+    lib.deltakv_kv_append.restype = ctypes.c_int
+    lib.deltakv_kv_decode_attention.argtypes = [vp, kvc, vp, i64p, vp, i64p, vp, vp, i32, f32, vp, sz, vp]
+    lib.deltakv_kv_decode_attention.restype = ctypes.c_int
+    lib.deltakv_kv_evict.argtypes = [vp, kvc, vp, i32, i32, vp, vp, vp, vp, i32, vp, vp, sz, vp]
+    lib.deltakv_kv_evict.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -347,6 +368,169 @@ def decode_attention_paged(p: Plan, seq_lens, max_len: int, q, pool, n_pages: in
     _check("deltakv_decode_attention_paged", lib.deltakv_decode_attention_paged(
         p.handle, _ptr(seq_lens), int(max_len), _ptr(q), qs, _ptr(pool), int(n_pages), _ptr(page_table), max_pages,
         _ptr(W3), _ptr(b3), _ptr(W4), _ptr(b4), _ptr(out), os_, _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+# ---- plain paged cache
+
+
+def kv_pool_layout(p: Plan, n_pages: int, tokens_per_page: int, max_len: int) -> dict:
+    """deltakv_kv_pool_layout: plane offsets and bytes of a pool of n_pages
+    pages, and the workspace bytes of kv calls with lengths up to max_len."""
+    lay = _KvLayout()
+    _check("deltakv_kv_pool_layout", load_library().deltakv_kv_pool_layout(
+        p.handle, int(n_pages), int(tokens_per_page), int(max_len), ctypes.byref(lay)))
+    return {f: getattr(lay, f) for f, _ in _KvLayout._fields_}
+
+
+def alloc_kv_pool(p: Plan, n_pages: int, tokens_per_page: int, device="cuda"):
+    """A zeroed pool [2 (K, V), n_pages, tokens_per_page, d_h]."""
+    kv_pool_layout(p, n_pages, tokens_per_page, 1)  # refuses sizes that are not built
+    return torch.zeros((2, n_pages, tokens_per_page, p.cfg.d_h), dtype=p.cfg.torch_dtype(), device=device)
+
+
+def alloc_kv_workspace(p: Plan, max_len: int, weights: bool = False, device="cuda"):
+    """Workspace of the kv calls with lengths up to max_len; `weights`: also
+    for kv_decode_attention with weights."""
+    lay = kv_pool_layout(p, 1, 16, max_len)
+    return torch.zeros(lay["weights_workspace_bytes" if weights else "workspace_bytes"], dtype=torch.uint8,
+                       device=device)
+
+
+def _kv_tensor(name, t, dtype, shape, device):
+    """Refuse what the kernels would misread: another type, shape or layout,
+    or a tensor that does not live where the cache does."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if t.dtype is not dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)}, got {t.dtype} {list(t.shape)}"
+                         f"{'' if t.is_contiguous() else ' (not contiguous)'}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    return t.data_ptr()
+
+
+def _stride(t, i, one=0):
+    """Stride of dimension i; `one` where it has one element, whose stride
+    (torch leaves it arbitrary) is never used."""
+    return t.stride(i) if t.shape[i] > 1 else one
+
+
+class KVCache:
+    """One layer's plain paged cache (deltakv_kv_cache): pool [2, n_pages,
+    tokens_per_page, d_h] in the plan's type, page_table int32 [B, H,
+    max_pages], lens int32 [B, H] (valid rows).  Holds the tensors; the caller
+    may change their contents between calls."""
+
+    def __init__(self, p: Plan, pool, page_table, lens):
+        c = p.cfg
+        if not isinstance(pool, torch.Tensor) or pool.dim() != 4:
+            raise ValueError("pool must be a tensor [2, n_pages, tokens_per_page, d_h]")
+        n_pages, page = int(pool.shape[1]), int(pool.shape[2])
+        kv_pool_layout(p, n_pages, page, 1)
+        self.device = pool.device
+        _kv_tensor("pool", pool, c.torch_dtype(), (2, n_pages, page, c.d_h), self.device)
+        max_pages = _page_table(p, page_table)
+        _kv_tensor("page_table", page_table, torch.int32, (c.batch, c.kv_heads, max_pages), self.device)
+        _kv_tensor("lens", lens, torch.int32, (c.batch, c.kv_heads), self.device)
+        self.plan, self.pool, self.page_table, self.lens = p, pool, page_table, lens
+        self._c = _KvCache(pool.data_ptr(), n_pages, page, page_table.data_ptr(), max_pages, lens.data_ptr(), 0)
+
+    def _ref(self, p, max_len, workspace):
+        if self.plan is not p and self.plan.cfg != p.cfg:
+            raise ValueError("the cache belongs to a plan of another configuration")
+        if self.device.type != "cuda" or self.device.index != torch.cuda.current_device():
+            raise ValueError(f"the cache is on {self.device}, not on the current CUDA device")
+        if workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
+        # a view of its own for each call: max_len belongs to the call
+        return _KvCache(self._c.pool, self._c.n_pages, self._c.tokens_per_page, self._c.page_table,
+                        self._c.max_pages, self._c.lens, max_len)
+
+
+def _kv_meta(name, t, dtype, p, device):
+    """A [B, H, cap] array of row weights or positions; (pointer, cap)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a tensor [{p.cfg.batch}, {p.cfg.kv_heads}, cap]")
+    return _kv_tensor(name, t, dtype, (p.cfg.batch, p.cfg.kv_heads, t.shape[2]), device), int(t.shape[2])
+
+
+def kv_append(p: Plan, cache: KVCache, max_len: int, K, V, workspace, n_tokens=None, first_pos=None, weights=None,
+              pos=None, token_weights=None, stream=None):
+    """deltakv_kv_append: K, V [B, H, n_new, d_h] (any batch/head/token
+    strides, contiguous last dim) become the last rows of each (sequence,
+    kv-head); cache.lens already counts them.  n_tokens int32 [B]: tokens each
+    sequence brings (default n_new).  pos int32 and weights float32 [B, H, cap]
+    get first_pos[b] + t and token_weights [B, H, n_new] (0 where None)."""
+    c, B, H = p.cfg, p.cfg.batch, p.cfg.kv_heads
+    dev = cache.device
+    if K.dim() != 4 or V.shape != K.shape or tuple(K.shape[:2]) != (B, H) or K.shape[3] != c.d_h:
+        raise ValueError(f"K and V must have shape [{B}, {H}, n_new, {c.d_h}], got {list(K.shape)}, {list(V.shape)}")
+    if K.dtype is not c.torch_dtype() or V.dtype is not c.torch_dtype() or K.device != dev or V.device != dev:
+        raise ValueError(f"K and V must be {c.torch_dtype()} on {dev}")
+    n_new = int(K.shape[2])
+    if n_new == 0:
+        return
+    if K.stride(3) != 1 or V.stride(3) != 1:
+        raise ValueError("K and V must be contiguous in their last dimension")
+    if any(a != b for a, b, n in zip(K.stride(), V.stride(), K.shape) if n > 1):
+        raise ValueError("K and V must share strides")
+    nt = None if n_tokens is None else _kv_tensor("n_tokens", n_tokens, torch.int32, (B,), dev)
+    fp = None if first_pos is None else _kv_tensor("first_pos", first_pos, torch.int32, (B,), dev)
+    tw = None if token_weights is None else _kv_tensor("token_weights", token_weights, torch.float32, (B, H, n_new), dev)
+    w = pp = None
+    cap = cap_p = 0
+    if weights is not None:
+        w, cap = _kv_meta("weights", weights, torch.float32, p, dev)
+    if pos is not None:
+        pp, cap_p = _kv_meta("pos", pos, torch.int32, p, dev)
+    if w is not None and pp is not None and cap != cap_p:
+        raise ValueError(f"weights and pos must have the same cap, got {cap} and {cap_p}")
+    _check("deltakv_kv_append", load_library().deltakv_kv_append(
+        p.handle, cache._ref(p, int(max_len), workspace), n_new, K.data_ptr(), V.data_ptr(),
+        (ctypes.c_int64 * 3)(_stride(K, 0), _stride(K, 1), _stride(K, 2, c.d_h)), nt, fp, w, pp, max(cap, cap_p), tw, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def kv_decode_attention(p: Plan, cache: KVCache, max_len: int, q, out, workspace, weights=None, decay: float = 1.0,
+                        lse=None, stream=None):
+    """deltakv_kv_decode_attention: q [B, Hq, d_h] -> out [B, Hq, d_h]
+    float32, lse float32 [B, Hq]; weights float32 [B, H, cap] gather each
+    row's attention weight (decay w + p)."""
+    c, dev = p.cfg, cache.device
+    shape = (c.batch, c.q_heads, c.d_h)
+    if tuple(q.shape) != shape or q.dtype is not c.torch_dtype() or q.stride(2) != 1 or q.device != dev:
+        raise ValueError(f"q must be {c.torch_dtype()} {list(shape)} on {dev}, contiguous in its last dimension")
+    if tuple(out.shape) != shape or out.dtype is not torch.float32 or out.stride(2) != 1 or out.device != dev:
+        raise ValueError(f"out must be float32 {list(shape)} on {dev}, contiguous in its last dimension")
+    w, cap = (None, 0) if weights is None else _kv_meta("weights", weights, torch.float32, p, dev)
+    ls = None if lse is None else _kv_tensor("lse", lse, torch.float32, shape[:2], dev)
+    _check("deltakv_kv_decode_attention", load_library().deltakv_kv_decode_attention(
+        p.handle, cache._ref(p, int(max_len), workspace), q.data_ptr(),
+        (ctypes.c_int64 * 2)(_stride(q, 0), _stride(q, 1)), out.data_ptr(),
+        (ctypes.c_int64 * 2)(_stride(out, 0), _stride(out, 1)), ls, w, cap, float(decay), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def kv_evict(p: Plan, cache: KVCache, max_len: int, budget, weights, pos, workspace, n_first: int = 0,
+             n_recent: int = 0, lens_out=None, weights_out=None, pos_out=None, stream=None):
+    """deltakv_kv_evict: keep budget int32 [B, H] rows of each (sequence,
+    kv-head), those of the first n_first and last n_recent positions and then
+    the largest weights.  lens_out, weights_out and pos_out default to
+    cache.lens, weights and pos (in place)."""
+    B, H, dev = p.cfg.batch, p.cfg.kv_heads, cache.device
+    lens_out = cache.lens if lens_out is None else lens_out
+    weights_out = weights if weights_out is None else weights_out
+    pos_out = pos if pos_out is None else pos_out
+    w, cap = _kv_meta("weights", weights, torch.float32, p, dev)
+    shape = (B, H, cap)
+    ptrs = [_kv_tensor("pos", pos, torch.int32, shape, dev),
+            _kv_tensor("weights_out", weights_out, torch.float32, shape, dev),
+            _kv_tensor("pos_out", pos_out, torch.int32, shape, dev)]
+    _check("deltakv_kv_evict", load_library().deltakv_kv_evict(
+        p.handle, cache._ref(p, int(max_len), workspace),
+        _kv_tensor("budget", budget, torch.int32, (B, H), dev), int(n_first), int(n_recent), w, *ptrs, cap,
+        _kv_tensor("lens_out", lens_out, torch.int32, (B, H), dev), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream(stream)))
 
 

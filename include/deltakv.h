@@ -342,13 +342,125 @@ deltakv_status deltakv_decode_attention_paged(deltakv_plan_t plan, const int32_t
                                               void* workspace, size_t workspace_bytes,
                                               deltakv_stream_t stream);
 
+/* ---- Plain paged cache: K and V rows as they are, in pages of a shared pool.
+ * What a model holds before (or beside) compression: layers or recent tokens
+ * kept whole, the full cache a compressed one is compared with, and caches
+ * made smaller by dropping tokens.  A page is tokens_per_page consecutive rows
+ * of one (sequence, kv-head); lengths are per (sequence, kv-head).
+ *
+ * Pool layout: the K plane, then the V plane, each [n_pages][tokens_per_page]
+ * [d_h] of the plan's element type (bfloat16 with DELTAKV_BF16_CODE4).  Row r
+ * of a (sequence, kv-head) is row r mod tokens_per_page of the pool page that
+ * entry r / tokens_per_page of its page-table row names. */
+typedef struct {
+    size_t k_offset, v_offset;        /* bytes from the pool's base */
+    size_t pool_bytes;
+    size_t workspace_bytes;           /* kv_append, kv_evict, kv_decode_attention without weights */
+    size_t weights_workspace_bytes;   /* kv_decode_attention with weights (a logit per row and query head) */
+} deltakv_kv_layout;
+
+/* One layer's plain paged cache as the kv calls take it; every pointer is the
+ * caller's.  The calls check what they read through it: a page index outside
+ * [0, n_pages) is never followed (its rows are skipped) and a length outside
+ * [0, max_len] is read as 0; both are reported as DELTAKV_ERR_DEVICE_BOUNDS.
+ * Entries of page_table past a pair's last page are not read.  Calls that
+ * write rows need each of a table's pages to be its only holder's. */
+typedef struct {
+    void* pool;                 /* device, 16-byte aligned, pool_bytes */
+    int32_t n_pages;
+    int32_t tokens_per_page;    /* 16, 32, 64, 128 or 256 */
+    const int32_t* page_table;  /* device [B][H][max_pages] */
+    int32_t max_pages;          /* at least ceil(max_len / tokens_per_page) */
+    const int32_t* lens;        /* device [B][H]: valid rows */
+    int32_t max_len;            /* host, 1 <= max_len <= max_T: no entry of lens is larger */
+} deltakv_kv_cache;
+
+/* Sizes of a pool of n_pages pages and of the workspace of kv calls with
+ * lengths up to max_len.  No device work.  Errors: INVALID_ARG; UNSUPPORTED
+ * (another tokens_per_page, or 2^31 rows and more in a pool). */
+deltakv_status deltakv_kv_pool_layout(deltakv_plan_t plan, int32_t n_pages, int32_t tokens_per_page,
+                                      int32_t max_len, deltakv_kv_layout* out);
+
+/* Write new tokens into the pages: the n_b = n_tokens[b] (NULL: n_new) first
+ * tokens of K, V of sequence b become the rows lens - n_b .. lens - 1 of each
+ * of its kv-heads (lens already counts them).  Rows before and behind them
+ * are left as they were.
+ *   n_new      : tokens in K and V, 0 <= n_new (0 launches nothing)
+ *   K, V       : device, element (b, h, t, e) at base + b*strides[0] +
+ *                h*strides[1] + t*strides[2] + e, as for deltakv_compress
+ *   n_tokens   : device int32 [B] or NULL; a count outside [0, n_new], or
+ *                larger than the pair's length, writes nothing for the pair
+ *                and is reported as DEVICE_BOUNDS
+ *   pos        : device int32 [B][H][cap] or NULL: the new rows' positions
+ *                are written, first_pos[b] + t
+ *   first_pos  : device int32 [B], position of sequence b's first new token
+ *                (NULL with pos NULL only)
+ *   weights    : device float32 [B][H][cap] or NULL: the new rows' weights
+ *                are set to token_weights (0 where that is NULL)
+ *   token_weights : device float32 [B][H][n_new] or NULL (attention weight a
+ *                token got before it came here, as from a prefill)
+ *   cap        : row stride of weights and pos, >= max_len (ignored if both
+ *                are NULL)
+ *   workspace  : deltakv_kv_layout.workspace_bytes (its error word only).
+ * Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, CUDA. */
+deltakv_status deltakv_kv_append(deltakv_plan_t plan, const deltakv_kv_cache* cache, int32_t n_new,
+                                 const void* K, const void* V, const int64_t kv_strides[3],
+                                 const int32_t* n_tokens, const int32_t* first_pos, float* weights,
+                                 int32_t* pos, int32_t cap, const float* token_weights,
+                                 void* workspace, size_t workspace_bytes, deltakv_stream_t stream);
+
+/* Attention of one new token per sequence over its plain paged rows: for query
+ * head hq of kv-head h,
+ *   out = sum_r p_r V_r,  p = softmax_r(q . K_r / sqrt(d_h)),  r < lens[b][h]
+ * (out = 0 and lse = -inf where a pair holds no row), and with weights also
+ *   weights[b][h][r] = decay weights[b][h][r] + sum over the pair's heads of p_r
+ * for the same rows, the accumulated attention weight deltakv_kv_evict ranks
+ * by.  Rows are split over the whole GPU whatever their lengths and joined by
+ * their log-sum-exp; the result does not depend on timing.
+ *   q, out     : as for deltakv_decode_attention
+ *   lse        : device float32 [B][Hq] or NULL: log sum_r exp(logit_r)
+ *   weights    : device float32 [B][H][cap] or NULL; cap >= max_len
+ *   decay      : >= 0 and finite (1: plain sums); ignored without weights
+ *   workspace  : workspace_bytes, or weights_workspace_bytes with weights, of
+ *                the layout for this max_len; scratch.
+ * Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, CUDA. */
+deltakv_status deltakv_kv_decode_attention(deltakv_plan_t plan, const deltakv_kv_cache* cache, const void* q,
+                                           const int64_t q_strides[2], float* out, const int64_t out_strides[2],
+                                           float* lse, float* weights, int32_t cap, float decay, void* workspace,
+                                           size_t workspace_bytes, deltakv_stream_t stream);
+
+/* Drop the rows with the least accumulated attention weight.  Of the n rows
+ * of a (sequence, kv-head), m = min(n, max(budget[b][h], n_first + n_recent))
+ * are kept: those whose position is below n_first or among the last n_recent
+ * positions (pos > max pos - n_recent), then those with the largest weights
+ * (NaN ranks lowest; ties to the lower row).  Kept rows below m stay where
+ * they are; kept rows at or past m move, in order, into the dropped rows below
+ * m, so that rows 0 .. m-1 are the kept ones and only what has to move moves
+ * (attention does not depend on the rows' order; pos says which token a row
+ * is).  K and V rows move in place.  Pages past ceil(m / tokens_per_page) are
+ * free afterwards.
+ *   budget     : device int32 [B][H]; a negative entry drops nothing and is
+ *                reported as DEVICE_BOUNDS
+ *   n_first, n_recent : >= 0, their sum <= max_T
+ *   weights, pos : device float32 and int32 [B][H][cap], cap >= max_len
+ *   weights_out, pos_out : device [B][H][cap], rows 0 .. m-1 are written;
+ *                each may be its input (in place), else must not overlap it
+ *   lens_out   : device int32 [B][H], set to m; may be cache->lens
+ *   workspace  : workspace_bytes of the layout for this max_len.
+ * A pair with a page index out of range among its first n rows is left whole
+ * (m = n) and reported.  Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, CUDA. */
+deltakv_status deltakv_kv_evict(deltakv_plan_t plan, const deltakv_kv_cache* cache, const int32_t* budget,
+                                int32_t n_first, int32_t n_recent, const float* weights, const int32_t* pos,
+                                float* weights_out, int32_t* pos_out, int32_t cap, int32_t* lens_out,
+                                void* workspace, size_t workspace_bytes, deltakv_stream_t stream);
+
 /* Synchronise `stream`, read and clear the error word that the kernels latch
  * in `workspace`, and return DELTAKV_OK, DEVICE_TIMEOUT or DEVICE_BOUNDS. */
 deltakv_status deltakv_device_status(deltakv_plan_t plan, void* workspace,
                                      deltakv_stream_t stream);
 
 /* Tracing: every call that launches kernels (compress, append, the decode
- * calls, pages_from_cache, reconstruct) opens an NVTX range named after the
+ * calls, pages_from_cache, reconstruct, the kv calls) opens an NVTX range named after the
  * call for its duration, so a tool that records NVTX ranges shows each
  * call's kernels under its name.  Without such a tool the ranges cost a
  * pointer test each.

@@ -1,0 +1,516 @@
+"""Plain paged cache on the GPU: append, decode attention and eviction against
+plain implementations in 64 bits (kv_util)."""
+import numpy as np
+import pytest
+import torch
+
+from decode_attention_strided_b200 import deltakv as dkv
+from kv_util import KvCase, Setup, attend64, attend_bounds, evict64
+
+pytestmark = pytest.mark.gpu
+
+BOUNDS = 7  # ERR_DEVICE_BOUNDS
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from decode_attention_strided_b200 import build
+    build.build()
+
+
+# ---- attention
+
+def _attend(s: Setup, weights=True, decay=1.0, lse=True, max_len=None):
+    c = s.c
+    out = torch.full((c.B, c.Hq, c.d), float("nan"), device="cuda")
+    ls = torch.full((c.B, c.Hq), float("nan"), device="cuda") if lse else None
+    w = s.w.cuda() if weights else None
+    dkv.kv_decode_attention(s.p, s.cache, max_len or c.n, s.q.cuda(), out, s.ws, weights=w, decay=decay, lse=ls)
+    return out, ls, w
+
+
+def _check_attend(s: Setup, out, lse, w, decay=1.0, pairs=None):
+    c = s.c
+    out = out.cpu().double().numpy()
+    w0 = s.w.double().numpy()
+    for b in range(c.B):
+        for h in range(c.H):
+            if pairs is not None and (b, h) not in pairs:
+                continue
+            n, g0 = c.lens[b][h], h * c.G
+            q = s.q[b, g0:g0 + c.G].double().numpy()
+            K, V = s.K[b, h].double().numpy(), s.V[b, h].double().numpy()
+            ref, ref_lse, p = attend64(q, K, V)
+            got = out[b, g0:g0 + c.G]
+            if n == 0:
+                assert (got == 0).all()
+                if lse is not None:
+                    assert (lse[b, g0:g0 + c.G] == -np.inf).all()
+                if w is not None:
+                    assert torch.equal(w[b, h].cpu(), s.w[b, h])
+                continue
+            tol, tol_lse, rel = attend_bounds(q, K, V, p)
+            err = np.abs(got - ref)
+            assert (err <= tol).all(), (b, h, n, float((err / tol).max()))
+            if lse is not None:
+                e = np.abs(lse[b, g0:g0 + c.G].cpu().double().numpy() - ref_lse)
+                assert (e <= tol_lse).all(), (b, h, n, float((e / tol_lse).max()))
+            if w is not None:
+                want = decay * w0[b, h, :n] + p.sum(axis=0)
+                e = np.abs(w[b, h, :n].cpu().double().numpy() - want)
+                lim = (rel[:, None] * p).sum(axis=0) + 2.0 ** -22 * want
+                assert (e <= lim).all(), (b, h, n, float((e / lim).max()))
+                assert torch.equal(w[b, h, n:].cpu(), s.w[b, h, n:])  # rows behind the last
+
+
+ATTEND = [
+    ("one_row", KvCase([[1]], 1)),
+    ("sixteen", KvCase([[16, 15, 17]], 3, page=16)),
+    ("g8_d64", KvCase([[1000, 3], [64, 129]], 16, d=64, page=32)),
+    ("g8_d128", KvCase([[1000, 31], [255, 257]], 16, page=256)),
+    ("g3", KvCase([[700, 1, 0]], 9, page=128)),
+    ("g5_d64", KvCase([[333], [2047]], 5, d=64, page=16)),
+    ("g7", KvCase([[130, 64]], 14)),
+    ("empty_between", KvCase([[0, 200], [0, 0], [77, 0]], 8)),
+    ("all_empty", KvCase([[0, 0]], 4, max_len=40)),
+    ("long", KvCase([[20011, 5]], 8)),
+    ("many_pairs", KvCase([[(37 * i + 11 * h) % 300 for h in range(8)] for i in range(40)], 32)),
+    ("peaked", KvCase([[3001, 900]], 8, scale=6.0)),
+    ("f32", KvCase([[1000, 3], [64, 129]], 16, dtype=dkv.F32)),
+    ("f32_d64_g1", KvCase([[2049, 16, 0]], 3, d=64, page=16, dtype=dkv.F32)),
+    ("f32_g3", KvCase([[5003, 100]], 6, page=32, dtype=dkv.F32, scale=3.0)),
+    ("code4_plan", KvCase([[100, 300]], 8, dtype=dkv.BF16_CODE4)),
+]
+
+
+@pytest.mark.parametrize("name,case", ATTEND, ids=[n for n, _ in ATTEND])
+@pytest.mark.parametrize("weights", [False, True], ids=["plain", "weights"])
+def test_attend(name, case, weights):
+    s = Setup(case)
+    decay = 0.75 if case.seed == 0 and case.G % 2 else 1.0
+    out, lse, w = _attend(s, weights, decay)
+    assert dkv.device_status(s.p, s.ws) == 0
+    _check_attend(s, out, lse, w, decay)
+
+
+def test_attend_is_deterministic_and_optional_outputs_change_nothing():
+    s = Setup(KvCase([[9001, 40], [300, 2000]], 8))
+    first = _attend(s)
+    for _ in range(3):
+        again = _attend(s)
+        for a, b in zip(first, again):
+            assert torch.equal(a, b)
+    out, _, _ = _attend(s, weights=False, lse=False)
+    assert torch.equal(out, first[0])
+
+
+def test_attend_max_len_above_the_lengths():
+    """max_len bounds the lengths; it need not be the longest."""
+    s = Setup(KvCase([[50, 300]], 4, max_len=4000))
+    out, lse, w = _attend(s)
+    assert dkv.device_status(s.p, s.ws) == 0
+    _check_attend(s, out, lse, w)
+
+
+def test_attend_strided_queries_and_outputs():
+    c = KvCase([[500, 17], [64, 900]], 8)
+    s = Setup(c)
+    q = torch.zeros(c.Hq, c.B, 2 * c.d, dtype=c.torch_dtype(), device="cuda")
+    q[:, :, :c.d] = s.q.cuda().transpose(0, 1)
+    buf = torch.full((c.Hq, c.B, c.d + 4), 7.0, device="cuda")
+    out = buf[:, :, :c.d].transpose(0, 1)
+    dkv.kv_decode_attention(s.p, s.cache, c.n, q[:, :, :c.d].transpose(0, 1), out, s.ws)
+    assert dkv.device_status(s.p, s.ws) == 0
+    _check_attend(s, out, None, None)
+    assert (buf[:, :, c.d:] == 7.0).all()
+
+
+def test_attend_infinities_and_nan_in_valid_rows_stay_in_their_pair():
+    c = KvCase([[100, 100], [90, 30]], 4)
+    s = Setup(c)
+    ids = s.table_host
+    s.pool[0, ids[0, 0, 1], 3, 5] = float("nan")
+    s.pool[1, ids[1, 1, 0], 2, 7] = float("inf")
+    out, lse, w = _attend(s)
+    assert dkv.device_status(s.p, s.ws) == 0
+    _check_attend(s, out, lse, w, pairs=[(0, 1), (1, 0)])
+    assert torch.isnan(out[0, :2]).all()
+    got = out[1, 2:4]
+    assert torch.isinf(got[:, 7]).all() and torch.isfinite(got[:, :7]).all() and torch.isfinite(got[:, 8:]).all()
+
+
+def test_attend_bad_page_is_skipped_and_reported():
+    c = KvCase([[300, 200], [300, 64]], 8)
+    s = Setup(c)
+    for bad in (-1, s.pool.shape[1]):
+        t = s.table_host.clone()
+        t[0, 0, 1] = bad
+        s.table.copy_(t)
+        out, lse, w = _attend(s)
+        assert dkv.device_status(s.p, s.ws) == BOUNDS
+        assert dkv.device_status(s.p, s.ws) == 0
+        K, V = s.K[0, 0], s.V[0, 0]
+        s.K[0, 0] = torch.cat([K[:64], K[128:]])
+        s.V[0, 0] = torch.cat([V[:64], V[128:]])
+        saved, s.w = s.w, s.w.clone()
+        c.lens[0][0] = 236
+        # the skipped rows get no weight; the check below has the others in order
+        wr = w.clone()
+        assert torch.equal(wr[0, 0, 64:128].cpu(), saved[0, 0, 64:128])
+        wr[0, 0, :236] = torch.cat([w[0, 0, :64], w[0, 0, 128:300]])
+        wr[0, 0, 236:] = saved[0, 0, 236:].cuda()
+        s.w[0, 0, :236] = torch.cat([saved[0, 0, :64], saved[0, 0, 128:300]])
+        _check_attend(s, out, lse, wr)
+        s.w, c.lens[0][0] = saved, 300
+        s.K[0, 0], s.V[0, 0] = K, V
+
+
+def test_attend_all_pages_bad_gives_an_empty_row():
+    s = Setup(KvCase([[40, 50]], 2))
+    s.table[0, 0] = -5
+    out, lse, w = _attend(s)
+    assert dkv.device_status(s.p, s.ws) == BOUNDS
+    assert (out[0, 0] == 0).all() and lse[0, 0] == -float("inf")
+    assert torch.equal(w[0, 0].cpu(), s.w[0, 0])
+    _check_attend(s, out, lse, w, pairs=[(0, 1)])
+
+
+@pytest.mark.parametrize("bad", [-1, 301, 2**31 - 1])
+def test_attend_bad_length_is_an_empty_row_and_reported(bad):
+    c = KvCase([[300, 200], [299, 64]], 8)
+    s = Setup(c)
+    s.lens[1, 0] = bad
+    out, lse, w = _attend(s)
+    assert dkv.device_status(s.p, s.ws) == BOUNDS
+    assert (out[1, :4] == 0).all() and (lse[1, :4] == -float("inf")).all()
+    assert torch.equal(w[1, 0].cpu(), s.w[1, 0])
+    _check_attend(s, out, lse, w, pairs=[(0, 0), (0, 1), (1, 1)])
+
+
+def test_attend_on_another_stream_and_in_two_graphs():
+    """Captured and replayed with lengths that change between replays; two
+    graphs, each with a workspace of its own, replayed on two streams."""
+    cases = [KvCase([[3000, 120]], 8, seed=1), KvCase([[77, 2500]], 8, seed=2)]
+    ss = [Setup(c) for c in cases]
+    qs = [s.q.cuda() for s in ss]
+    outs = [torch.empty(1, 8, 128, device="cuda") for _ in ss]
+    ws = [s.w.cuda() for s in ss]
+    graphs = []
+    streams = [torch.cuda.Stream() for _ in ss]
+    torch.cuda.synchronize()
+    for i, s in enumerate(ss):
+        with torch.cuda.stream(streams[i]):
+            dkv.kv_decode_attention(s.p, s.cache, s.c.n, qs[i], outs[i], s.ws, weights=ws[i])
+            torch.cuda.synchronize()
+            _check_attend(s, outs[i], None, ws[i])
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=streams[i]):
+                dkv.kv_decode_attention(s.p, s.cache, s.c.n, qs[i], outs[i], s.ws, weights=ws[i])
+            graphs.append(g)
+    for lens in ([[3000, 120], [77, 2500]], [[1, 0], [60, 1999]], [[2999, 64], [0, 2500]]):
+        for i, s in enumerate(ss):
+            s.lens.copy_(torch.tensor([lens[i]], dtype=torch.int32))
+            ws[i].copy_(s.w)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for i in range(2):
+                with torch.cuda.stream(streams[i]):
+                    graphs[i].replay()
+        torch.cuda.synchronize()
+        for i, s in enumerate(ss):
+            assert dkv.device_status(s.p, s.ws) == 0
+            t = Setup.__new__(Setup)
+            t.__dict__.update(s.__dict__)
+            t.c = KvCase([lens[i]], 8, max_len=s.c.n)
+            t.K = {k: v[:lens[i][k[1]]] for k, v in s.K.items()}
+            t.V = {k: v[:lens[i][k[1]]] for k, v in s.V.items()}
+            _check_attend(t, outs[i], None, None)
+            total = float((ws[i] - s.w.cuda()).sum())
+            heads = sum(4 for n in lens[i] if n)
+            assert abs(total - 3 * heads) < 1e-3 * max(1, heads)
+
+
+# ---- append
+
+def _append_ref(s, K, V, counts, first_pos, tok_w, w, pos, pool):
+    c = s.c
+    pool, w, pos = pool.clone(), w.clone(), pos.clone()
+    for b in range(c.B):
+        n = counts[b]
+        for h in range(c.H):
+            for t in range(n):
+                r = c.lens[b][h] - n + t
+                pg = int(s.table_host[b, h, r // c.page])
+                pool[0, pg, r % c.page] = K[b, h, t]
+                pool[1, pg, r % c.page] = V[b, h, t]
+                w[b, h, r] = 0.0 if tok_w is None else tok_w[b, h, t]
+                pos[b, h, r] = first_pos[b] + t
+    return pool, w, pos
+
+
+def _same(a, b):
+    """Bit for bit (NaN included)."""
+    v = torch.int32 if a.dtype == torch.float32 else torch.int16 if a.dtype == torch.bfloat16 else a.dtype
+    return torch.equal(a.cpu().view(v), b.cpu().view(v))
+
+
+APPEND = [
+    ("one_token", KvCase([[1, 64], [65, 300]], 2), 1, None),
+    ("block", KvCase([[40, 100], [90, 40], [200, 128]], 2, page=16), 40, [40, 0, 17]),
+    ("f32", KvCase([[33, 47]], 2, page=32, dtype=dkv.F32), 33, None),
+    ("f32_d64", KvCase([[33, 47], [9, 8]], 2, d=64, page=16, dtype=dkv.F32), 33, [30, 8]),
+    ("d64", KvCase([[130, 131]], 2, d=64, page=256), 129, None),
+]
+
+
+@pytest.mark.parametrize("layout", ["bhtd", "bthd"])
+@pytest.mark.parametrize("name,case,n_new,counts", APPEND, ids=[a[0] for a in APPEND])
+def test_append(name, case, n_new, counts, layout):
+    s = Setup(case)
+    c = case
+    g = torch.Generator().manual_seed(5)
+    shape = (c.B, c.H, n_new, c.d) if layout == "bhtd" else (c.B, n_new, c.H, c.d)
+    K, V = (torch.randn(*shape, generator=g).to(c.torch_dtype()) for _ in range(2))
+    if layout == "bthd":
+        K, V = K.transpose(1, 2), V.transpose(1, 2)
+    cnt = counts or [n_new] * c.B
+    first = [1000 * b + 3 for b in range(c.B)]
+    tok_w = torch.rand(c.B, c.H, n_new, generator=g)
+    cap = c.n + 5
+    w0 = torch.rand(c.B, c.H, cap, generator=g)
+    pos0 = torch.full((c.B, c.H, cap), -9, dtype=torch.int32)
+    pool0 = s.pool.cpu()
+    for tw in (tok_w, None):
+        s.pool.copy_(pool0)
+        w, pos = w0.cuda(), pos0.cuda()
+        # .cuda() keeps the strides of a transposed view
+        dkv.kv_append(s.p, s.cache, c.n, K.cuda(), V.cuda(), s.ws,
+                      n_tokens=None if counts is None else torch.tensor(counts, dtype=torch.int32, device="cuda"),
+                      first_pos=torch.tensor(first, dtype=torch.int32, device="cuda"), weights=w, pos=pos,
+                      token_weights=None if tw is None else tw.cuda())
+        assert dkv.device_status(s.p, s.ws) == 0
+        pool, wr, pr = _append_ref(s, K, V, cnt, first, tw, w0, pos0, pool0)
+        assert _same(s.pool, pool) and _same(w, wr) and _same(pos, pr)
+    # without the optional arrays only the rows change
+    s.pool.copy_(pool0)
+    dkv.kv_append(s.p, s.cache, c.n, K.cuda(), V.cuda(), s.ws,
+                  n_tokens=None if counts is None else torch.tensor(counts, dtype=torch.int32, device="cuda"))
+    assert _same(s.pool, _append_ref(s, K, V, cnt, first, None, w0, pos0, pool0)[0])
+
+
+def test_append_reports_bad_counts_lengths_and_pages():
+    c = KvCase([[40, 100], [90, 70], [30, 20], [64, 65]], 2, page=16)
+    s = Setup(c)
+    K = torch.zeros(4, 2, 25, 128, dtype=torch.bfloat16, device="cuda")
+    pool0 = s.pool.cpu()
+    # sequence 0: negative; 1: above n_new; 2: above the second head's length only; 3: fine
+    s.lens.copy_(s.lens_host)
+    cnt = torch.tensor([-1, 26, 25, 2], dtype=torch.int32, device="cuda")
+    dkv.kv_append(s.p, s.cache, c.n, K, K, s.ws, n_tokens=cnt)
+    assert dkv.device_status(s.p, s.ws) == BOUNDS
+    want = pool0.clone()
+    for b, h, r0, n in ((2, 0, 5, 25), (3, 0, 62, 2), (3, 1, 63, 2)):
+        for r in range(r0, r0 + n):
+            want[:, s.table_host[b, h, r // 16], r % 16] = 0
+    assert _same(s.pool, want)
+    # a length out of range and a page out of range write nothing there
+    s.pool.copy_(pool0)
+    s.lens[0, 0] = c.n + 1
+    s.table[3, 1, 4] = s.pool.shape[1]  # row 64
+    cnt = torch.tensor([1, 0, 0, 2], dtype=torch.int32, device="cuda")
+    dkv.kv_append(s.p, s.cache, c.n, K, K, s.ws, n_tokens=cnt)
+    assert dkv.device_status(s.p, s.ws) == BOUNDS
+    want = pool0.clone()
+    for b, h, r in ((0, 1, 99), (3, 0, 62), (3, 0, 63), (3, 1, 63)):
+        want[:, s.table_host[b, h, r // 16], r % 16] = 0
+    assert _same(s.pool, want)
+
+
+# ---- evict
+
+def _evict_check(s, budget, n_first, n_recent, w, pos, in_place, whole=()):
+    """Run an eviction and compare every byte with the definition."""
+    c = s.c
+    cap = w.shape[2]
+    pool0 = s.pool.cpu()
+    wd, pd = w.cuda(), pos.cuda()
+    bud = torch.tensor(budget, dtype=torch.int32, device="cuda")
+    if in_place:
+        wo, po, lo = wd, pd, s.lens
+        w_want, p_want = w.clone(), pos.clone()
+    else:
+        wo, po = torch.full_like(wd, -3.0), torch.full_like(pd, -4)
+        lo = torch.full_like(s.lens, -5)
+        w_want, p_want = wo.cpu(), po.cpu()
+    dkv.kv_evict(s.p, s.cache, c.n, bud, wd, pd, s.ws, n_first=n_first, n_recent=n_recent, lens_out=lo,
+                 weights_out=wo, pos_out=po)
+    st = dkv.device_status(s.p, s.ws)
+    pool_want = pool0.clone()
+    l_want = torch.zeros(c.B, c.H, dtype=torch.int32)
+    for b in range(c.B):
+        for h in range(c.H):
+            n = c.lens[b][h]
+            if (b, h) in whole:
+                m, src = n, np.arange(n)
+            else:
+                m, src = evict64(n, budget[b][h], n_first, n_recent, w[b, h, :n].numpy(), pos[b, h, :n].numpy())
+            l_want[b, h] = m
+            src = torch.from_numpy(src).long()
+            w_want[b, h, :m] = w[b, h][src]
+            p_want[b, h, :m] = pos[b, h][src]
+            for r in range(m):
+                q = int(src[r])
+                if q != r:
+                    pool_want[:, s.table_host[b, h, r // c.page], r % c.page] = \
+                        pool0[:, s.table_host[b, h, q // c.page], q % c.page]
+    assert torch.equal(lo.cpu(), l_want)
+    assert _same(po, p_want)
+    assert _same(wo, w_want)
+    assert _same(s.pool, pool_want)
+    if not in_place:
+        assert _same(wd, w) and _same(pd, pos)
+    return st
+
+
+def _meta(c, seed, kind, cap=None):
+    g = torch.Generator().manual_seed(seed)
+    cap = cap or c.n
+    if kind == "random":
+        w = torch.exp(torch.randn(c.B, c.H, cap, generator=g) * 3)
+    elif kind == "equal":
+        w = torch.full((c.B, c.H, cap), 0.25)
+    elif kind == "few":      # many ties at every threshold
+        w = torch.randint(0, 4, (c.B, c.H, cap), generator=g).float() * 0.5
+    elif kind == "close":    # differ in the last bits only
+        w = (torch.randint(0, 50, (c.B, c.H, cap), generator=g) + 0x3f800000).to(torch.int32).view(torch.float32)
+    else:                    # zeros of both signs, infinities, NaN of both signs, subnormals, negatives
+        pick = torch.tensor([0.0, -0.0, float("inf"), -float("inf"), float("nan"), -float("nan"), 1e-42, -1e-42,
+                             3.4e38, -1.0, 1.0])
+        w = pick[torch.randint(0, len(pick), (c.B, c.H, cap), generator=g)]
+    pos = torch.stack([torch.randperm(3 * cap, generator=g)[:cap] for _ in range(c.B * c.H)])
+    return w.contiguous(), pos.view(c.B, c.H, cap).to(torch.int32).contiguous()
+
+
+EVICT = [
+    ("one_out", KvCase([[101, 64, 17]], 3, page=16), 1, 0, 4),
+    ("half", KvCase([[1000, 999], [3, 2500]], 2), 2, 2, 10),
+    ("guard_only", KvCase([[500, 20]], 2, page=32), 8, 5, 30),
+    ("long", KvCase([[20000, 30011]], 2, d=64, page=128), 5, 4, 100),
+    ("f32", KvCase([[300, 700, 0]], 3, dtype=dkv.F32), 2, 1, 0),
+    ("f32_d64", KvCase([[1, 2, 130]], 3, d=64, page=16, dtype=dkv.F32), 2, 0, 0),
+]
+
+
+@pytest.mark.parametrize("in_place", [False, True], ids=["apart", "in_place"])
+@pytest.mark.parametrize("kind", ["random", "equal", "few", "close", "special"])
+@pytest.mark.parametrize("name,case,div,first,recent", EVICT, ids=[e[0] for e in EVICT])
+def test_evict(name, case, div, first, recent, kind, in_place):
+    c = case
+    s = Setup(c)
+    w, pos = _meta(c, 3, kind, c.n + 3)
+    budget = [[(n - 1 if div == 1 else n // div) for n in row] for row in c.lens]
+    assert _evict_check(s, budget, first, recent, w, pos, in_place) == 0
+
+
+def test_evict_budgets_of_nothing_everything_and_out_of_range():
+    c = KvCase([[300, 301, 302, 303]], 4)
+    s = Setup(c)
+    w, pos = _meta(c, 4, "random")
+    assert _evict_check(s, [[0, 303, 2**31 - 1, 1]], 0, 0, w, pos, False) == 0
+    s = Setup(c)
+    assert _evict_check(s, [[-1, 303, 4, -2**31]], 0, 0, w, pos, False, whole=[(0, 0), (0, 3)]) == BOUNDS
+
+
+def test_evict_bad_pages_and_lengths_leave_the_pair_whole():
+    c = KvCase([[300, 200, 129]], 3)
+    s = Setup(c)
+    w, pos = _meta(c, 4, "random")
+    s.table[0, 1, 3] = -7  # only rows 192 .. 199
+    assert _evict_check(s, [[100, 100, 100]], 0, 0, w, pos, False, whole=[(0, 1)]) == BOUNDS
+    s = Setup(c)
+    s.lens[0, 2] = 301
+    s.c = KvCase([[300, 200, 0]], 3)
+    assert _evict_check(s, [[100, 100, 100]], 0, 0, w, pos, False) == BOUNDS
+
+
+def test_evict_repeated_positions_stay_in_bounds():
+    """Positions that repeat guard more rows than the budget holds: the guarded
+    rows rank first, the lowest rows of them are kept."""
+    c = KvCase([[500, 400]], 2)
+    s = Setup(c)
+    w, pos = _meta(c, 4, "random")
+    pos[:] = 7
+    assert _evict_check(s, [[50, 60]], 4, 10, w, pos, False) == 0
+
+
+# ---- together
+
+@pytest.mark.parametrize("dtype", [dkv.BF16, dkv.F32], ids=["bf16", "f32"])
+def test_serving_steps_under_a_budget(dtype):
+    """Prompts appended, then steps of append, decode with weights and evict
+    back to the budget: every step's attention against 64 bits over the rows
+    the definition keeps, ranked by the weights the GPU had."""
+    B, H, Hq, d, page, budget, steps = 2, 2, 8, 128, 16, 96, 14
+    prompt = [90, 41]
+    cap = 256
+    dt = torch.float32 if dtype == dkv.F32 else torch.bfloat16
+    g = torch.Generator().manual_seed(9)
+    p = dkv.plan(dkv.Config(batch=B, kv_heads=H, q_heads=Hq, d_h=d, max_T=cap, stride_s=8, k=2, d_c=16, hidden=128,
+                            dtype=dtype))
+    per = cap // page
+    pool = dkv.alloc_kv_pool(p, B * H * per, page)
+    table = torch.randperm(B * H * per, generator=g).to(torch.int32).view(B, H, per).cuda()
+    lens = torch.tensor(prompt, dtype=torch.int32, device="cuda")[:, None].repeat(1, H)
+    cache = dkv.KVCache(p, pool, table, lens)
+    ws = dkv.alloc_kv_workspace(p, cap, weights=True)
+    w = torch.zeros(B, H, cap, device="cuda")
+    pos = torch.zeros(B, H, cap, dtype=torch.int32, device="cuda")
+    bud = torch.full((B, H), budget, dtype=torch.int32, device="cuda")
+    next_pos = torch.zeros(B, dtype=torch.int32, device="cuda")
+    cnt = torch.tensor(prompt, dtype=torch.int32, device="cuda")
+    toks = {}
+    K = torch.randn(B, H, max(prompt), d, generator=g).to(dt)
+    V = torch.randn(B, H, max(prompt), d, generator=g).to(dt)
+    dkv.kv_append(p, cache, cap, K.cuda(), V.cuda(), ws, n_tokens=cnt, first_pos=next_pos, weights=w, pos=pos)
+    next_pos += cnt
+    model = {}
+    for b in range(B):
+        for h in range(H):
+            for t in range(prompt[b]):
+                toks[b, h, t] = (K[b, h, t], V[b, h, t])
+            model[b, h] = list(range(prompt[b]))
+    for step in range(steps):
+        lens += 1
+        K = torch.randn(B, H, 1, d, generator=g).to(dt)
+        V = torch.randn(B, H, 1, d, generator=g).to(dt)
+        dkv.kv_append(p, cache, cap, K.cuda(), V.cuda(), ws, first_pos=next_pos, weights=w, pos=pos)
+        q = torch.randn(B, Hq, d, generator=g).to(dt)
+        out = torch.empty(B, Hq, d, device="cuda")
+        w_before = w.clone()
+        dkv.kv_decode_attention(p, cache, cap, q.cuda(), out, ws, weights=w, decay=0.9)
+        w_mid, pos_mid = w.cpu(), pos.cpu()
+        dkv.kv_evict(p, cache, cap, bud, w, pos, ws, n_first=2, n_recent=8)
+        assert dkv.device_status(p, ws) == 0
+        for b in range(B):
+            for h in range(H):
+                now = prompt[b] + step
+                toks[b, h, now] = (K[b, h, 0], V[b, h, 0])
+                rows = model[b, h] + [now]
+                assert pos_mid[b, h, :len(rows)].tolist() == rows
+                Kr = torch.stack([toks[b, h, t][0] for t in rows]).double().numpy()
+                Vr = torch.stack([toks[b, h, t][1] for t in rows]).double().numpy()
+                qh = q[b, h * 4:h * 4 + 4].double().numpy()
+                ref, _, pr = attend64(qh, Kr, Vr)
+                tol, _, rel = attend_bounds(qh, Kr, Vr, pr)
+                assert (np.abs(out[b, h * 4:h * 4 + 4].cpu().double().numpy() - ref) <= tol).all()
+                want = 0.9 * w_before[b, h, :len(rows)].cpu().double().numpy() + pr.sum(axis=0)
+                lim = (rel[:, None] * pr).sum(axis=0) + 2.0 ** -22 * want
+                assert (np.abs(w_mid[b, h, :len(rows)].double().numpy() - want) <= lim).all()
+                m, src = evict64(len(rows), budget, 2, 8, w_mid[b, h, :len(rows)].numpy(),
+                                 pos_mid[b, h, :len(rows)].numpy())
+                model[b, h] = [rows[i] for i in src]
+                assert int(lens[b, h]) == m
+                assert torch.equal(w[b, h, :m].cpu(), w_mid[b, h][torch.from_numpy(src).long()])
+        next_pos += 1
