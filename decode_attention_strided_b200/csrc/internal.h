@@ -226,12 +226,14 @@ struct KvView {
   }
   // valid rows of a pair; a length out of range is none
   __device__ int len(int64_t bh) const {
-    const int n = lens[bh];
+    const int n = __ldcg(lens + bh);  // L2 only: the kernels may start before the grid ahead of them has ended
     return n < 0 || n > max_len ? 0 : n;
   }
+  // the page-table entry of row r of pair bh (unchecked)
+  __device__ int32_t page(int64_t bh, int r) const { return __ldcg(ptab + bh * max_pages + (r >> page_log)); }
   // pool row of row r of pair bh, or -1 where its page is out of range
   __device__ int64_t row(int64_t bh, int r) const {
-    const int32_t pg = ptab[bh * max_pages + (r >> page_log)];
+    const int32_t pg = page(bh, r);
     if (pg < 0 || pg >= n_pages) {
       report((uint32_t)pg);
       return -1;
@@ -243,7 +245,7 @@ struct KvView {
 
 // Workspace regions of the kv calls (bytes from the base; each after the
 // error word).
-constexpr int kKvMaxGrid = 2 * kNumSMs;  // CTAs of the attention's split
+constexpr int kKvMaxGrid = kNumSMs;  // CTAs of the attention's split (one per SM)
 // floats of one partial result (a multiple of 16 bytes)
 __host__ __device__ constexpr int kv_part_floats(int G, int d_h) { return G * d_h + 2 * kMaxG; }
 struct KvWorkspace {

@@ -60,16 +60,17 @@ __device__ __forceinline__ int64_t units_of(int len) { return (len + kUnit - 1) 
 
 // Total units, and the pair that holds the first unit of this CTA's range
 // (its number and its first unit), by a block scan over the lengths.  Every
-// thread returns the same values.  Lengths out of range are reported here.
-__device__ Cut locate(const KvView& c, int64_t BH, int64_t& bh0, int64_t& s0) {
-  __shared__ int64_t sh_warp[kWarps];
-  __shared__ int64_t sh_bh, sh_s;
+// thread returns the same values; sh: kLocateWords of shared memory, free again
+// on return.  Lengths out of range are reported here.
+constexpr int kLocateWords = kWarps + 2;
+__device__ Cut locate(const KvView& c, int64_t BH, int64_t* sh, int64_t& bh0, int64_t& s0) {
+  int64_t *sh_warp = sh, &sh_bh = sh[kWarps], &sh_s = sh[kWarps + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t per = (BH + kThreads - 1) / kThreads;
   const int64_t b0 = min(BH, tid * per), b1 = min(BH, b0 + per);
   int64_t sum = 0;
   for (int64_t b = b0; b < b1; ++b) {
-    const int n = c.lens[b];
+    const int n = __ldcg(c.lens + b);
     if (n < 0 || n > c.max_len) c.report((uint32_t)n);
     sum += units_of(c.len(b));
   }
@@ -103,6 +104,7 @@ __device__ Cut locate(const KvView& c, int64_t BH, int64_t& bh0, int64_t& s0) {
   __syncthreads();
   bh0 = sh_bh;
   s0 = sh_s;
+  __syncthreads();
   return cut;
 }
 
@@ -152,78 +154,539 @@ __device__ __forceinline__ void finish_segment(const AttendArgs& a, const Merge<
   }
 }
 
+// ---- the tiles of one warp
+// A warp takes every eighth unit of its CTA's range and streams its rows
+// through a ring of shared-memory stages of its own: lane 0 issues one bulk
+// copy of a stage's K rows and one of its V rows (rows of a page are
+// contiguous, and a stage never leaves its page), an mbarrier per stage tells
+// when they have landed, and the stage is refilled as soon as its rows are in
+// registers.  No other warp takes part, so the warps drift freely between the
+// segments' ends.
 template <typename E, int DH>
-__global__ void __launch_bounds__(kThreads) kv_attend_kernel(AttendArgs a) {
-  constexpr int NV = DH / 32;
-  __shared__ Merge<DH> sm;
+struct Ring {
+  static constexpr int kRowBytes = DH * (int)sizeof(E);
+  static constexpr int kRows = kRowBytes == 512 ? 8 : 16;       // rows per stage
+  static constexpr int kSub = kUnit / kRows;                    // stages per unit
+  static constexpr int kHalf = kRows * kRowBytes;               // bytes of K (or V) per stage
+  static constexpr int kStages = 24 * 1024 / (2 * kHalf);       // 3 stages of 8 KB, or 6 of 4 KB
+};
+
+template <typename E, int DH>
+struct AttendSmem {
+  alignas(128) char ring[kWarps][Ring<E, DH>::kStages][2][Ring<E, DH>::kHalf];
+  Merge<DH> merge;
+  // float32 rows: the weights of a stage's rows, then the rescaling factors
+  float p[kWarps][sizeof(E) == 4 ? Ring<E, DH>::kRows + 1 : 1][kMaxG];
+  uint64_t bar[kWarps][Ring<E, DH>::kStages];
+};
+
+// Where a warp's next stage comes from; all lanes hold the same values.
+struct Cursor {
+  int64_t bh, s;    // the pair, and its first unit
+  int64_t u;        // the unit (of the flat list)
+  int len, sub;
+  int32_t page;     // its page-table entry, loaded one stage ahead
+};
+
+template <typename E, int DH>
+struct Loader {
+  using R = Ring<E, DH>;
+  const KvView& c;
+  AttendSmem<E, DH>& sm;
+  const int warp, lane;
+  const int64_t u_end;
+  Cursor k;
+  int put = 0, get = 0;   // stages issued and taken
+  uint32_t good = 0;      // bit i: stage i's page is in range
+  bool dead = false;      // a wait ran out: nothing more is issued
+
+  __device__ Loader(const KvView& c_, AttendSmem<E, DH>& s_, int w, int l, int64_t bh, int64_t s, int64_t u,
+                    int64_t e)
+      : c(c_), sm(s_), warp(w), lane(l), u_end(e) {
+    k.bh = bh;
+    k.s = s;
+    k.u = u;
+    k.sub = 0;
+    k.len = u < e ? c.len(bh) : 0;
+    seek();
+  }
+  // move to the pair that holds unit k.u and load its page-table entry
+  __device__ __forceinline__ void seek() {
+    if (k.u >= u_end) return;
+    while (k.u >= k.s + units_of(k.len)) {
+      k.s += units_of(k.len);
+      k.len = c.len(++k.bh);
+    }
+    k.page = c.page(k.bh, (int)(k.u - k.s) * kUnit);
+  }
+  __device__ __forceinline__ void issue() {
+    if (k.u >= u_end || dead) return;
+    const int st = put % R::kStages;
+    const bool ok = k.page >= 0 && k.page < c.n_pages;
+    good = ok ? good | (1u << st) : good & ~(1u << st);
+    if (lane == 0) {
+      uint64_t* bar = &sm.bar[warp][st];
+      if (ok) {
+        const int r = (int)(k.u - k.s) * kUnit + k.sub * R::kRows;
+        const int64_t off = (((int64_t)k.page << c.page_log) + (r & ((1 << c.page_log) - 1))) * R::kRowBytes;
+        sm100::mbar_arrive_expect_tx(bar, 2 * R::kHalf);
+        sm100::bulk_load(sm.ring[warp][st][0], c.k + off, R::kHalf, bar);
+        sm100::bulk_load(sm.ring[warp][st][1], c.v + off, R::kHalf, bar);
+      } else {
+        c.report((uint32_t)k.page);
+        sm100::mbar_arrive(bar);
+      }
+    }
+    ++put;
+    if (++k.sub == R::kSub) {
+      k.sub = 0;
+      k.u += kWarps;
+      seek();
+    }
+  }
+  // Wait for the next stage; its number, or -1 where it holds no rows (a page
+  // out of range, or a wait that ran out).
+  __device__ __forceinline__ int take() {
+    const int st = get % R::kStages;
+    if (!dead) {
+      const bool got = sm100::mbar_wait_drain(&sm.bar[warp][st], (get / R::kStages) & 1);
+      if (__any_sync(0xffffffffu, !got)) {
+        dead = true;
+        if (lane == 0) latch_error(c.err, DELTAKV_ERR_DEVICE_TIMEOUT, 0u);
+      }
+    }
+    if (dead) return -1;
+    ++get;
+    return good >> st & 1 ? st : -1;
+  }
+  // on the way out after a wait ran out: no copy may land in shared memory
+  // that the CTA no longer owns
+  __device__ void drain() {
+    if (dead)
+      for (int i = get; i < put; ++i) sm100::mbar_wait_drain(&sm.bar[warp][i % R::kStages], (i / R::kStages) & 1);
+  }
+};
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transpose of an 8x8 matrix of 16-bit elements held two per lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// z becomes NaN in a half where v's is infinite or NaN, else keeps its value.
+__device__ __forceinline__ void note_nonfinite(uint32_t& z, uint32_t v) {
+  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(z) : "r"(v), "r"(0u));
+}
+// v with its infinite and NaN halves zero
+__device__ __forceinline__ uint32_t finite_halves(uint32_t v) {
+  const uint32_t t = (v & 0x7f807f80u) + 0x00800080u;  // bit 15 of a half: its exponent is all ones
+  return v & ~((t >> 15 & 0x00010001u) * 0xffffu);
+}
+
+// bfloat16 rows on the tensor cores, 16 rows a step.  Lane (gr, t) = (lane /
+// 4, lane % 4).  Rows are the M side of both products and the pair's query
+// heads (at most 8, zero beyond G) the N side, so no product is wasted on
+// padding: X[row][head] = K Q^T, and O[dim][head] += V^T P.
+//  - X: the contraction index is permuted so that a lane's four 32-bit
+//    operands of two k-steps are one 16-byte word of its K row (the same word
+//    of the query row), read straight from the row.
+//  - O: the rows of M are permuted so that a lane's words of V rows 2t, 2t+1,
+//    2t+8, 2t+9 hold its operands once the two rows of a pair are interleaved
+//    (byte permutes); P comes out of X's accumulators by an 8x8 transpose.
+//  - P in three bfloat16 terms (24 bits of it): with one, each weight would
+//    carry 2^-8 into a float32 result.  The extra products cost nothing here:
+//    the tensor pipe is far from full.  An infinite V element must meet the
+//    first term only (the others may be zero or negative), so the others take
+//    V with such elements zeroed where a step has any.
+//  - A step's products go into zeroed accumulators that are then added to the
+//    running ones in float32: the tensor core's own additions may truncate,
+//    which over thousands of steps would bias the sums.
+template <int DH>
+struct Bf16Rows {
+  static constexpr int kW = DH / 32;       // 16-byte words of a row per lane and product (K), of DH / 8 in all
+  static constexpr int kM = DH / 16;       // M tiles of O
+  uint32_t q[kW][4];
+  float o[kM][4], m[2], l[2];
+
+  __device__ __forceinline__ void start(const AttendArgs& a, int64_t b, int h, int lane) {
+    const int gr = lane >> 2, t = lane & 3;
+    const auto* qp = static_cast<const __nv_bfloat16*>(a.q) + b * a.qsb + (int64_t)(h * a.G + gr) * a.qsh;
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (gr < a.G) v = __ldcg(reinterpret_cast<const uint4*>(qp) + i * 4 + t);
+      q[i][0] = v.x;
+      q[i][1] = v.y;
+      q[i][2] = v.z;
+      q[i][3] = v.w;
+    }
+#pragma unroll
+    for (int j = 0; j < kM; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+  }
+
+  // Rows [r, r + 16) of the pair, of which `valid` count; xl: their logits in
+  // global memory, or null.  `refill` is called once the rows are in registers.
+  template <typename F>
+  __device__ __forceinline__ void step(const AttendArgs& a, const char* ks, const char* vs, float* p_smem, int valid,
+                                       float* xl, int lane, F refill) {
+    const int gr = lane >> 2, t = lane & 3;
+    float x0[4] = {0.f, 0.f, 0.f, 0.f}, x1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+      const uint4 ka = *reinterpret_cast<const uint4*>(ks + gr * DH * 2 + (i * 4 + t) * 16);
+      const uint4 kb = *reinterpret_cast<const uint4*>(ks + (gr + 8) * DH * 2 + (i * 4 + t) * 16);
+      mma_bf16(x0, ka.x, kb.x, ka.y, kb.y, q[i][0], q[i][1]);
+      mma_bf16(x1, ka.z, kb.z, ka.w, kb.w, q[i][2], q[i][3]);
+    }
+    // V rows 2t, 2t + 1, 2t + 8, 2t + 9: words gr (and gr + 8)
+    constexpr int kH = DH / 64;
+    uint4 v[kH][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 2 * t + (i & 1) + (i >> 1) * 8;
+#pragma unroll
+      for (int w = 0; w < kH; ++w) v[w][i] = *reinterpret_cast<const uint4*>(vs + row * DH * 2 + (w * 8 + gr) * 16);
+    }
+    __syncwarp();
+    refill();
+    float x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = (x0[i] + x1[i]) * a.scale2;
+    if (valid < kUnit) {
+      // rows behind the last: whatever the page holds must not count (0 x NaN)
+      if (gr >= valid) x[0] = x[1] = -INFINITY;
+      if (gr + 8 >= valid) x[2] = x[3] = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (2 * t + (i & 1) + (i >> 1) * 8 >= valid)
+#pragma unroll
+          for (int w = 0; w < kH; ++w) v[w][i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (xl) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = gr + (i >> 1) * 8, g = 2 * t + (i & 1);
+        if (row < valid && g < a.G) xl[(int64_t)row * a.G + g] = x[i];
+      }
+    }
+    float f[2], p[4];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float mx = fmaxf(x[c], x[c + 2]);
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+      mx = fmaxf(mx, m[c]);
+      const float mu = mx == -INFINITY ? 0.f : mx;
+      f[c] = exp2f(m[c] - mu);
+      m[c] = mx;
+      p[c] = exp2f(x[c] - mu);
+      p[c + 2] = exp2f(x[c + 2] - mu);
+      l[c] = fmaf(l[c], f[c], p[c] + p[c + 2]);
+    }
+    uint32_t nz[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int w = 0; w < kH; ++w)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        note_nonfinite(nz[0], v[w][i].x);
+        note_nonfinite(nz[1], v[w][i].y);
+        note_nonfinite(nz[2], v[w][i].z);
+        note_nonfinite(nz[3], v[w][i].w);
+      }
+    // the halves are zero or NaN
+    const bool odd = __any_sync(0xffffffffu, ((nz[0] | nz[1] | nz[2] | nz[3]) & 0x7fff7fffu) != 0u);
+    uint32_t pb[3][2];
+#pragma unroll
+    for (int s = 0; s < 3; ++s)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const uint32_t w = pack_bf16(p[2 * hf], p[2 * hf + 1]);
+        p[2 * hf] -= lo_f(w);
+        p[2 * hf + 1] -= hi_f(w);
+        pb[s][hf] = transpose8(w);
+      }
+#pragma unroll
+    for (int j = 0; j < kM; ++j) {
+      // M rows gr and gr + 8 of tile j: dims 8 gr + j and 64 + 8 gr + j (DH 128), 8 gr + 2 j and 8 gr + 2 j + 1 (64)
+      uint32_t av[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int up = i & 1, pr = i >> 1;  // a0: rows gr, tokens 2t..; a1: rows gr + 8; a2, a3: tokens 2t + 8..
+        const uint32_t* ra = reinterpret_cast<const uint32_t*>(&v[kH == 2 ? up : 0][2 * pr]);
+        const uint32_t* rb = reinterpret_cast<const uint32_t*>(&v[kH == 2 ? up : 0][2 * pr + 1]);
+        const int word = kH == 2 ? j >> 1 : j;
+        const bool high = kH == 2 ? j & 1 : up;
+        av[i] = __byte_perm(ra[word], rb[word], high ? 0x7632 : 0x5410);
+      }
+      uint32_t lv[4] = {av[0], av[1], av[2], av[3]};
+      if (odd)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lv[i] = finite_halves(lv[i]);
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
+      mma_bf16(c, lv[0], lv[1], lv[2], lv[3], pb[2][0], pb[2][1]);
+      mma_bf16(c, lv[0], lv[1], lv[2], lv[3], pb[1][0], pb[1][1]);
+      mma_bf16(c, av[0], av[1], av[2], av[3], pb[0][0], pb[0][1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[j][i] = fmaf(o[j][i], f[i & 1], c[i]);
+    }
+  }
+
+  __device__ __forceinline__ void finish(Merge<DH>& mg, int warp, int lane) {
+    const int gr = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      l[c] += __shfl_xor_sync(0xffffffffu, l[c], 4);
+      l[c] += __shfl_xor_sync(0xffffffffu, l[c], 8);
+      l[c] += __shfl_xor_sync(0xffffffffu, l[c], 16);
+      if (gr == 0) {
+        mg.m[warp][2 * t + c] = m[c];
+        mg.l[warp][2 * t + c] = l[c];
+      }
+      float* op = mg.o[warp][2 * t + c] + gr * 8;
+      if constexpr (DH == 128) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+          for (int j = 0; j < 8; j += 4)
+            *reinterpret_cast<float4*>(op + w * 64 + j) =
+                make_float4(o[j][2 * w + c], o[j + 1][2 * w + c], o[j + 2][2 * w + c], o[j + 3][2 * w + c]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; j += 2)
+          *reinterpret_cast<float4*>(op + 2 * j) = make_float4(o[j][c], o[j][2 + c], o[j + 1][c], o[j + 1][2 + c]);
+      }
+    }
+  }
+};
+
+// float32 rows on the CUDA cores (float32 results leave no room for tf32's
+// 2^-11).  Logits: half a warp per row, a lane holds DH / 16 of the row's and
+// of every head's query elements in registers; the GP heads' partial sums are
+// reduced over the 16 lanes by exchange steps that leave each lane one head.
+// Outputs: a lane holds DH / 32 dims of all heads and reads the row's weights
+// from shared memory.  GP: heads rounded up to a power of two.
+template <int DH, int GP>
+struct F32Rows {
+  static constexpr int kQ = DH / 64;      // float4 of a row per lane (logits)
+  static constexpr int kD = DH / 32;      // dims per lane (outputs)
+  static constexpr int kRows = Ring<float, DH>::kRows;
+  float4 q[GP][kQ];
+  float o[GP][kD], m, l;
+
+  __device__ __forceinline__ static int head_of(int lane) {
+    int h = 0;
+    if constexpr (GP == 8) h = ((lane & 8) ? 4 : 0) | ((lane & 4) ? 2 : 0) | ((lane & 2) ? 1 : 0);
+    if constexpr (GP == 4) h = ((lane & 8) ? 2 : 0) | ((lane & 4) ? 1 : 0);
+    if constexpr (GP == 2) h = (lane & 8) ? 1 : 0;
+    return h;
+  }
+
+  __device__ __forceinline__ void start(const AttendArgs& a, int64_t b, int h, int lane) {
+    const auto* qp = static_cast<const float*>(a.q) + b * a.qsb + (int64_t)(h * a.G) * a.qsh;
+#pragma unroll
+    for (int g = 0; g < GP; ++g) {
+#pragma unroll
+      for (int i = 0; i < kQ; ++i)
+        q[g][i] = g < a.G ? __ldcg(reinterpret_cast<const float4*>(qp + g * a.qsh) + i * 16 + (lane & 15))
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kD; ++i) o[g][i] = 0.f;
+    }
+    m = -INFINITY;
+    l = 0.f;
+  }
+
+  template <typename F>
+  __device__ __forceinline__ void step(const AttendArgs& a, const char* ks, const char* vs, float* p_smem, int valid,
+                                       float* xl, int lane, F refill) {
+    const int half = lane >> 4, head = head_of(lane);
+    float x[kRows / 2];
+    float mx = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kRows / 2; ++j) {
+      const int row = 2 * j + half;
+      float v[GP];
+#pragma unroll
+      for (int g = 0; g < GP; ++g) v[g] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kQ; ++i) {
+        const float4 kx = *reinterpret_cast<const float4*>(ks + row * DH * 4 + (i * 16 + (lane & 15)) * 16);
+#pragma unroll
+        for (int g = 0; g < GP; ++g)
+          v[g] = fmaf(q[g][i].x, kx.x, fmaf(q[g][i].y, kx.y, fmaf(q[g][i].z, kx.z, fmaf(q[g][i].w, kx.w, v[g]))));
+      }
+      int n = GP;
+#pragma unroll
+      for (int s = 8; s > 0; s >>= 1) {
+        if (n > 1) {
+          n >>= 1;
+#pragma unroll
+          for (int i = 0; i < GP / 2; ++i)
+            if (i < n) {
+              const float keep = (lane & s) ? v[i + n] : v[i], send = (lane & s) ? v[i] : v[i + n];
+              v[i] = keep + __shfl_xor_sync(0xffffffffu, send, s);
+            }
+        } else {
+          v[0] += __shfl_xor_sync(0xffffffffu, v[0], s);
+        }
+      }
+      x[j] = row < valid ? v[0] * a.scale2 : -INFINITY;
+      if (xl && row < valid && head < a.G && (lane & (16 / GP - 1)) == 0) xl[(int64_t)row * a.G + head] = x[j];
+      mx = fmaxf(mx, x[j]);
+    }
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+    mx = fmaxf(mx, m);
+    const float mu = mx == -INFINITY ? 0.f : mx;
+    const float f = exp2f(m - mu);
+    m = mx;
+    l *= f;
+    __syncwarp();  // the last step's reads of p_smem
+#pragma unroll
+    for (int j = 0; j < kRows / 2; ++j) {
+      const float p = exp2f(x[j] - mu);
+      l += p;
+      p_smem[(2 * j + half) * kMaxG + head] = p;
+    }
+    p_smem[kRows * kMaxG + head] = f;
+    __syncwarp();
+    auto weights = [&](int row, float (&w)[GP]) {
+      const float* pp = p_smem + row * kMaxG;
+      if constexpr (GP >= 4) {
+#pragma unroll
+        for (int g = 0; g < GP; g += 4) {
+          const float4 t = *reinterpret_cast<const float4*>(pp + g);
+          w[g] = t.x;
+          w[g + 1] = t.y;
+          w[g + 2] = t.z;
+          w[g + 3] = t.w;
+        }
+      } else {
+#pragma unroll
+        for (int g = 0; g < GP; ++g) w[g] = pp[g];
+      }
+    };
+    float w[GP];
+    weights(kRows, w);
+#pragma unroll
+    for (int g = 0; g < GP; ++g)
+#pragma unroll
+      for (int i = 0; i < kD; ++i) o[g][i] *= w[g];
+#pragma unroll
+    for (int row = 0; row < kRows; ++row) {
+      if (row >= valid) break;  // rows behind the last hold anything
+      const float* vr = reinterpret_cast<const float*>(vs + row * DH * 4) + lane * kD;
+      float vx[kD];
+      if constexpr (kD == 4) {
+        const float4 t = *reinterpret_cast<const float4*>(vr);
+        vx[0] = t.x;
+        vx[1] = t.y;
+        vx[2] = t.z;
+        vx[3] = t.w;
+      } else {
+        const float2 t = *reinterpret_cast<const float2*>(vr);
+        vx[0] = t.x;
+        vx[1] = t.y;
+      }
+      weights(row, w);
+#pragma unroll
+      for (int g = 0; g < GP; ++g)
+#pragma unroll
+        for (int i = 0; i < kD; ++i) o[g][i] = fmaf(w[g], vx[i], o[g][i]);
+    }
+    __syncwarp();
+    refill();
+  }
+
+  __device__ __forceinline__ void finish(Merge<DH>& mg, int warp, int lane) {
+    l += __shfl_xor_sync(0xffffffffu, l, 16);
+    const int head = head_of(lane);
+    mg.m[warp][head] = m;
+    mg.l[warp][head] = l;
+#pragma unroll
+    for (int g = 0; g < GP; ++g)
+#pragma unroll
+      for (int i = 0; i < kD; ++i) mg.o[warp][g][lane * kD + i] = o[g][i];
+  }
+};
+
+// One CTA per SM, 8 warps, a 24 KB ring each: up to 192 KB of rows in flight
+// per SM, several times what the memory latency needs at full bandwidth.
+template <typename E, int DH, typename Rows>
+__global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(AttendArgs a) {
+  using R = Ring<E, DH>;
+  extern __shared__ __align__(128) char smem_raw[];
+  auto& sm = *reinterpret_cast<AttendSmem<E, DH>*>(smem_raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) {
+    for (int i = 0; i < R::kStages; ++i) sm100::mbar_init(&sm.bar[warp][i], 1);
+    sm100::fence_mbar_init();
+  }
+  __syncwarp();
+  sm100::grid_dep_wait();
+  sm100::grid_dep_launch();
   int64_t bh, s;
-  const Cut cut = locate(a.c, a.BH, bh, s);
+  const Cut cut = locate(a.c, a.BH, reinterpret_cast<int64_t*>(sm.merge.o), bh, s);
   if (cut.W == 0 || blockIdx.x >= cut.g) return;
   const int64_t u_end = cut.start(blockIdx.x + 1);
   int64_t u = cut.start(blockIdx.x);
+  int64_t mine = u + warp;  // this warp's next unit
+  Loader<E, DH> ld(a.c, sm, warp, lane, bh, s, mine, u_end);
+  for (int i = 0; i < R::kStages; ++i) ld.issue();
   for (bool first = true; u < u_end; first = false) {
     int len = a.c.len(bh);
     while (len == 0) len = a.c.len(++bh);
     const int64_t ub = units_of(len);
     const int64_t ua = u - s, ue = min(u_end - s, ub);
-    const int64_t b = bh / a.H;
-    const int h = (int)(bh % a.H);
-    float q[kMaxG][NV], acc[kMaxG][NV], m[kMaxG], l[kMaxG];
+    Rows rows;
+    rows.start(a, bh / a.H, (int)(bh % a.H), lane);
+    for (; mine < s + ue; mine += kWarps) {
 #pragma unroll
-    for (int g = 0; g < kMaxG; ++g) {
-      m[g] = -INFINITY;
-      l[g] = 0.f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        acc[g][i] = 0.f;
-        q[g][i] = g < a.G ? to_f(static_cast<const E*>(a.q)[b * a.qsb + (int64_t)(h * a.G + g) * a.qsh + lane * NV + i]) : 0.f;
-      }
-    }
-    for (int64_t t = ua + warp; t < ue; t += kWarps) {
-      for (int r = (int)t * kUnit; r < min(len, (int)t * kUnit + kUnit); ++r) {
-        const int64_t row = a.c.row(bh, r);
-        const E* kr = reinterpret_cast<const E*>(a.c.k) + row * DH + lane * NV;
-        const E* vr = reinterpret_cast<const E*>(a.c.v) + row * DH + lane * NV;
-        float kx[NV], vx[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          kx[i] = row < 0 ? 0.f : to_f(kr[i]);
-          vx[i] = row < 0 ? 0.f : to_f(vr[i]);
-        }
-#pragma unroll
-        for (int g = 0; g < kMaxG; ++g) {
-          if (g >= a.G) break;
-          float x = 0.f;
-#pragma unroll
-          for (int i = 0; i < NV; ++i) x = fmaf(q[g][i], kx[i], x);
-          x = row < 0 ? -INFINITY : warp_sum(x) * a.scale2;
-          if (a.logits && lane == 0) a.logits[(bh * a.c.max_len + r) * a.G + g] = x;
-          const float mn = fmaxf(m[g], x), mu = mn == -INFINITY ? 0.f : mn;
-          const float f = exp2f(m[g] - mu), p = exp2f(x - mu);
-          m[g] = mn;
-          l[g] = fmaf(l[g], f, p);
-#pragma unroll
-          for (int i = 0; i < NV; ++i) acc[g][i] = fmaf(acc[g][i], f, p * vx[i]);
+      for (int sub = 0; sub < R::kSub; ++sub) {
+        const int r = (int)(mine - s) * kUnit + sub * R::kRows;
+        const int valid = min(len - r, R::kRows);
+        const int st = ld.take();
+        float* xl = a.logits ? a.logits + (bh * a.c.max_len + r) * a.G : nullptr;
+        if (st >= 0) {
+          // (a stage of a unit's second half can lie behind the last row: valid <= 0)
+          rows.step(a, sm.ring[warp][st][0], sm.ring[warp][st][1], &sm.p[warp][0][0], valid, xl, lane,
+                    [&] { ld.issue(); });
+        } else {
+          if (xl)
+            for (int i = lane; i < valid * a.G; i += 32) xl[i] = -INFINITY;
+          __syncwarp();
+          ld.issue();
         }
       }
     }
-#pragma unroll
-    for (int g = 0; g < kMaxG; ++g) {
-      if (lane == 0) {
-        sm.m[warp][g] = m[g];
-        sm.l[warp][g] = l[g];
-      }
-#pragma unroll
-      for (int i = 0; i < NV; ++i) sm.o[warp][g][lane * NV + i] = acc[g][i];
-    }
+    rows.finish(sm.merge, warp, lane);
     __syncthreads();
-    finish_segment<DH>(a, sm, bh, ua == 0 && ue == ub, blockIdx.x, first ? 0 : 1);
+    finish_segment<DH>(a, sm.merge, bh, ua == 0 && ue == ub, blockIdx.x, first ? 0 : 1);
     __syncthreads();
     u = s + ue;
     s += ub;
     ++bh;
   }
+  ld.drain();
 }
 
 // Join the partial results of the pairs that several CTAs hold, and add the
@@ -233,9 +696,12 @@ template <int DH>
 __global__ void __launch_bounds__(kThreads) kv_join_kernel(AttendArgs a) {
   __shared__ float sh_f[kKvMaxGrid * kMaxG];  // factor of each part and head
   __shared__ float sh_L[kMaxG], sh_l[kMaxG];
+  __shared__ int64_t sh_loc[kLocateWords];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int64_t bh, s;
-  const Cut cut = locate(a.c, a.BH, bh, s);
+  // the lengths were final before the first kernel passed its own wait
+  const Cut cut = locate(a.c, a.BH, sh_loc, bh, s);
+  sm100::grid_dep_wait();
   // pairs without rows
   for (int64_t e = blockIdx.x; e < a.BH; e += gridDim.x) {
     if (a.c.len(e) != 0) continue;
@@ -331,17 +797,28 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(AttendArgs a) {
   }
 }
 
-template <typename E, int DH>
+template <typename E, int DH, typename Rows>
 cudaError_t launch_t(const Plan& p, const AttendArgs& a, int grid, cudaStream_t st) {
+  auto kern = kv_attend_kernel<E, DH, Rows>;
+  constexpr size_t smem = sizeof(AttendSmem<E, DH>);
+  static_assert(smem <= 227 * 1024, "shared memory of one CTA");
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
   {
     ProfScope ps(p, st, KID_KV_ATTEND);
-    kv_attend_kernel<E, DH><<<grid, kThreads, 0, st>>>(a);
+    e = launch_pdl(kern, grid, kThreads, smem, st, a);
   }
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   ProfScope ps(p, st, KID_KV_JOIN);
-  kv_join_kernel<DH><<<grid, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(kv_join_kernel<DH>, grid, kThreads, 0, st, a);
+}
+
+template <int DH>
+cudaError_t launch_f32(const Plan& p, const AttendArgs& a, int grid, cudaStream_t st) {
+  if (a.G == 1) return launch_t<float, DH, F32Rows<DH, 1>>(p, a, grid, st);
+  if (a.G == 2) return launch_t<float, DH, F32Rows<DH, 2>>(p, a, grid, st);
+  if (a.G <= 4) return launch_t<float, DH, F32Rows<DH, 4>>(p, a, grid, st);
+  return launch_t<float, DH, F32Rows<DH, 8>>(p, a, grid, st);
 }
 
 }  // namespace
@@ -373,9 +850,9 @@ cudaError_t launch_kv_attend(const Plan& p, const KvView& c, const void* q, int6
   a.logits = w ? (float*)(base + L.logits) : nullptr;
   const int64_t most = a.BH * ceil_div64(c.max_len, kUnit);
   const int grid = (int)std::min<int64_t>(kKvMaxGrid, ceil_div64(most, kMinUnits));
-  if (p.bf16)
-    return cfg.d_h == 128 ? launch_t<__nv_bfloat16, 128>(p, a, grid, st) : launch_t<__nv_bfloat16, 64>(p, a, grid, st);
-  return cfg.d_h == 128 ? launch_t<float, 128>(p, a, grid, st) : launch_t<float, 64>(p, a, grid, st);
+  if (!p.bf16) return cfg.d_h == 128 ? launch_f32<128>(p, a, grid, st) : launch_f32<64>(p, a, grid, st);
+  return cfg.d_h == 128 ? launch_t<__nv_bfloat16, 128, Bf16Rows<128>>(p, a, grid, st)
+                        : launch_t<__nv_bfloat16, 64, Bf16Rows<64>>(p, a, grid, st);
 }
 
 }  // namespace dkv
