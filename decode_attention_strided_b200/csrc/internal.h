@@ -40,7 +40,7 @@ enum KernelId {
   KID_REFPACK = 0, KID_CAND_SIMT, KID_CAND_TC, KID_ENCODE_SIMT, KID_ENCODE_TC, KID_RECONSTRUCT, KID_DEC_REF,
   KID_DEC_PREP, KID_DEC_STREAM_SIMT, KID_DEC_STREAM_TC, KID_DEC_COMBINE, KID_DEC_FINAL,
   KID_APPEND_REFS, KID_APPEND_ROWS, KID_SPARSE_ATTEND, KID_SPARSE_MERGE, KID_SPARSE_SELECT,
-  KID_KV_APPEND, KID_KV_ATTEND, KID_KV_JOIN, KID_KV_SELECT, KID_KV_MOVE, KID_COUNT
+  KID_KV_APPEND, KID_KV_ATTEND, KID_KV_JOIN, KID_KV_WEIGHTS, KID_KV_SELECT, KID_KV_MOVE, KID_COUNT
 };
 const char* kernel_name(int id);
 
@@ -225,10 +225,11 @@ struct KvView {
     if (atomicCAS(err, 0u, (uint32_t)DELTAKV_ERR_DEVICE_BOUNDS) == 0u) err[1] = detail;
   }
   // valid rows of a pair; a length out of range is none
-  __device__ int len(int64_t bh) const {
-    const int n = __ldcg(lens + bh);  // L2 only: the kernels may start before the grid ahead of them has ended
-    return n < 0 || n > max_len ? 0 : n;
+  __device__ int raw_len(int64_t bh) const {
+    return __ldcg(lens + bh);  // L2 only: the kernels may start before the grid ahead of them has ended
   }
+  __device__ int checked(int n) const { return n < 0 || n > max_len ? 0 : n; }
+  __device__ int len(int64_t bh) const { return checked(raw_len(bh)); }
   // the page-table entry of row r of pair bh (unchecked)
   __device__ int32_t page(int64_t bh, int r) const { return __ldcg(ptab + bh * max_pages + (r >> page_log)); }
   // pool row of row r of pair bh, or -1 where its page is out of range
@@ -250,7 +251,7 @@ constexpr int kKvMaxGrid = kNumSMs;  // CTAs of the attention's split (one per S
 __host__ __device__ constexpr int kv_part_floats(int G, int d_h) { return G * d_h + 2 * kMaxG; }
 struct KvWorkspace {
   size_t part;    // attention: [kKvMaxGrid][2] partial results of kv_part_floats
-  size_t lse2;    // attention: [B H][G] float32 log-sum-exp in units of log2 of the pairs one CTA holds whole
+  size_t lse2;    // attention with weights: [B H][G] float32 log-sum-exp in units of log2
   size_t logits;  // attention with weights: [B H][max_len][G] float32, in units of log2
   size_t attend_end, weights_end;
   size_t count, hole, move;  // eviction: [B H] moves, their target and source rows [B H][max_len / 2]

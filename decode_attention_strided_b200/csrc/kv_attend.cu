@@ -15,6 +15,7 @@
 // partial results at most.  A second kernel joins them and adds the weights,
 // which need the joined (m, l) of each head.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "common.cuh"
@@ -33,8 +34,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 struct AttendArgs {
   KvView c;
-  int64_t BH;
-  int H, G;
+  int BH, H, G;
   const void* q;
   int64_t qsb, qsh;
   float* out;
@@ -48,64 +48,90 @@ struct AttendArgs {
   float* logits;  // [BH][max_len][G] or null
 };
 
-// The cut of the unit list into ranges.
+// The cut of the unit list into ranges: the first `rem` of them hold per + 1
+// units, the others per.  (The host refuses calls whose list could reach 2^31
+// units.)
 struct Cut {
-  int64_t W;  // units of all pairs
-  int64_t g;  // ranges (<= grid)
-  __device__ int64_t start(int64_t c) const { return c * W / g; }
-  __device__ int64_t cta_of(int64_t u) const { return ((u + 1) * g - 1) / W; }
+  int W, g;  // units of all pairs; ranges (0 where there is no unit)
+  int per, rem;
+  __device__ int start(int c) const { return c * per + min(c, rem); }
+  __device__ int range_of(int u) const {
+    const int head = rem * (per + 1);
+    return u < head ? u / (per + 1) : rem + (u - head) / per;
+  }
 };
 
-__device__ __forceinline__ int64_t units_of(int len) { return (len + kUnit - 1) / kUnit; }
+// A place in the unit list: a pair, its first unit and its length.
+struct Place {
+  int bh, s, len;
+};
 
-// Total units, and the pair that holds the first unit of this CTA's range
-// (its number and its first unit), by a block scan over the lengths.  Every
-// thread returns the same values; sh: kLocateWords of shared memory, free again
-// on return.  Lengths out of range are reported here.
-constexpr int kLocateWords = kWarps + 2;
-__device__ Cut locate(const KvView& c, int64_t BH, int64_t* sh, int64_t& bh0, int64_t& s0) {
-  int64_t *sh_warp = sh, &sh_bh = sh[kWarps], &sh_s = sh[kWarps + 1];
+__device__ __forceinline__ int units_of(int len) { return (len + kUnit - 1) / kUnit; }
+
+// The cut, and the pair that holds the first unit of range c, by a block scan
+// over the lengths.  Every thread returns the same values; sh: kLocateWords
+// of shared memory, free again on return.  Lengths out of range are reported
+// here; `empty` tells whether any pair holds no row.
+constexpr int kLocateWords = kWarps + 4;
+__device__ __forceinline__ Cut locate(const KvView& k, int BH, int c, int* sh, Place& at, bool& empty) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t per = (BH + kThreads - 1) / kThreads;
-  const int64_t b0 = min(BH, tid * per), b1 = min(BH, b0 + per);
-  int64_t sum = 0;
-  for (int64_t b = b0; b < b1; ++b) {
-    const int n = __ldcg(c.lens + b);
-    if (n < 0 || n > c.max_len) c.report((uint32_t)n);
-    sum += units_of(c.len(b));
+  const int per = (BH + kThreads - 1) / kThreads;
+  const int b0 = min(BH, tid * per), b1 = min(BH, b0 + per);
+  int sum = 0, none = 0, last = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int raw = k.raw_len(b);
+    last = k.checked(raw);
+    if (raw != last) k.report((uint32_t)raw);
+    none |= last == 0;
+    sum += units_of(last);
   }
-  int64_t inc = sum;
+  int inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += v;
   }
-  if (lane == 31) sh_warp[warp] = inc;
-  __syncthreads();
-  int64_t before = 0, W = 0;
+  if (lane == 31) sh[warp] = inc;
+  empty = __syncthreads_or(none) != 0;
+  int before = 0, W = 0;
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) {
-    if (i < warp) before += sh_warp[i];
-    W += sh_warp[i];
+    if (i < warp) before += sh[i];
+    W += sh[i];
   }
-  Cut cut{W, max((int64_t)1, min((int64_t)gridDim.x, (W + kMinUnits - 1) / kMinUnits))};
-  const int64_t target = cut.start(blockIdx.x);
-  int64_t s = before + inc - sum;
-  if (blockIdx.x < cut.g && target >= s && target < s + sum) {
-    int64_t b = b0;
-    for (; b < b1; ++b) {
-      const int64_t u = units_of(c.len(b));
-      if (target < s + u) break;
-      s += u;
+  Cut cut;
+  cut.W = W;
+  cut.g = min((int)kKvMaxGrid, (W + kMinUnits - 1) / kMinUnits);
+  cut.per = W / max(1, cut.g);
+  cut.rem = W - cut.per * cut.g;
+  if (c < cut.g) {
+    const int target = cut.start(c);
+    int s = before + inc - sum;
+    if (target >= s && target < s + sum) {
+      int b = b0;
+      if (per > 1)
+        for (;; ++b) {
+          last = k.len(b);
+          if (target < s + units_of(last)) break;
+          s += units_of(last);
+        }
+      sh[kWarps] = b;
+      sh[kWarps + 1] = s;
+      sh[kWarps + 2] = last;
     }
-    sh_bh = b;
-    sh_s = s;
   }
   __syncthreads();
-  bh0 = sh_bh;
-  s0 = sh_s;
+  at = Place{sh[kWarps], sh[kWarps + 1], sh[kWarps + 2]};
   __syncthreads();
   return cut;
+}
+
+// Move to the pair that holds unit u (at or after the present one).
+__device__ __forceinline__ void seek(const KvView& k, Place& at, int u) {
+  while (u >= at.s + units_of(at.len)) {
+    at.s += units_of(at.len);
+    at.len = k.len(++at.bh);
+  }
 }
 
 // One warp's running softmax over its rows, as partial results: m, l and o
@@ -116,36 +142,49 @@ struct Merge {
   float o[kWarps][kMaxG][DH];
 };
 
+// Four dims of one head's result; the thread of a head's first dims also
+// writes its log-sum-exp (-inf where no row counted).
+template <int DH>
+__device__ __forceinline__ void write_out(const AttendArgs& a, int bh, int b, int h, int g, int e, float m, float l,
+                                          float4 o) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<float4*>(a.out + b * a.osb + (int64_t)(h * a.G + g) * a.osh + e) =
+      make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  if (e == 0) {
+    const float L = m + log2f(l);
+    if (a.w) a.lse2[(int64_t)bh * a.G + g] = L;
+    if (a.lse) a.lse[(int64_t)bh * a.G + g] = kLn2 * L;
+  }
+}
+
 // Reduce the warps' parts of one segment and write them where they belong:
 // out and lse where the segment is the whole pair, else the partial slot.
 template <int DH>
-__device__ __forceinline__ void finish_segment(const AttendArgs& a, const Merge<DH>& sm, int64_t bh, bool whole,
-                                               int64_t cta, int slot) {
-  const int64_t b = bh / a.H;
-  const int h = (int)(bh % a.H);
-  float* part = a.part + (cta * 2 + slot) * (int64_t)kv_part_floats(a.G, DH);
-  for (int i = threadIdx.x; i < a.G * DH; i += kThreads) {
+__device__ __forceinline__ void finish_segment(const AttendArgs& a, const Merge<DH>& sm, int bh, bool whole, int slot) {
+  const int b = bh / a.H, h = bh - b * a.H;
+  float* part = a.part + (blockIdx.x * 2 + slot) * (int64_t)kv_part_floats(a.G, DH);
+  for (int i = threadIdx.x * 4; i < a.G * DH; i += kThreads * 4) {
     const int g = i / DH, e = i % DH;
     float m = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.m[w][g]);
     const float mu = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o = 0.f;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float f = exp2f(sm.m[w][g] - mu);
+      const float4 v = *reinterpret_cast<const float4*>(&sm.o[w][g][e]);
       l = fmaf(sm.l[w][g], f, l);
-      o = fmaf(sm.o[w][g][e], f, o);
+      o.x = fmaf(v.x, f, o.x);
+      o.y = fmaf(v.y, f, o.y);
+      o.z = fmaf(v.z, f, o.z);
+      o.w = fmaf(v.w, f, o.w);
     }
     if (whole) {
-      a.out[b * a.osb + (int64_t)(h * a.G + g) * a.osh + e] = l == 0.f ? 0.f : o / l;
-      if (e == 0) {
-        const float L = m + log2f(l);  // -inf where every row was skipped
-        a.lse2[bh * a.G + g] = L;
-        if (a.lse) a.lse[bh * a.G + g] = kLn2 * L;
-      }
+      write_out<DH>(a, bh, b, h, g, e, m, l, o);
     } else {
-      part[i] = o;
+      *reinterpret_cast<float4*>(part + i) = o;
       if (e == 0) {
         part[a.G * DH + g] = m;
         part[a.G * DH + kMaxG + g] = l;
@@ -180,68 +219,53 @@ struct AttendSmem {
   uint64_t bar[kWarps][Ring<E, DH>::kStages];
 };
 
-// Where a warp's next stage comes from; all lanes hold the same values.
-struct Cursor {
-  int64_t bh, s;    // the pair, and its first unit
-  int64_t u;        // the unit (of the flat list)
-  int len, sub;
-  int32_t page;     // its page-table entry, loaded one stage ahead
-};
-
 template <typename E, int DH>
 struct Loader {
   using R = Ring<E, DH>;
   const KvView& c;
   AttendSmem<E, DH>& sm;
-  const int warp, lane;
-  const int64_t u_end;
-  Cursor k;
+  const int warp, lane, u_end;
+  // the next stage's unit, its pair, its part of the unit and its page-table
+  // entry (loaded one unit ahead); all lanes hold the same values
+  int u, sub = 0;
+  Place at;
+  int32_t page;
   int put = 0, get = 0;   // stages issued and taken
   uint32_t good = 0;      // bit i: stage i's page is in range
   bool dead = false;      // a wait ran out: nothing more is issued
 
-  __device__ Loader(const KvView& c_, AttendSmem<E, DH>& s_, int w, int l, int64_t bh, int64_t s, int64_t u,
-                    int64_t e)
-      : c(c_), sm(s_), warp(w), lane(l), u_end(e) {
-    k.bh = bh;
-    k.s = s;
-    k.u = u;
-    k.sub = 0;
-    k.len = u < e ? c.len(bh) : 0;
-    seek();
+  __device__ Loader(const KvView& c_, AttendSmem<E, DH>& s_, int w, int l, Place p, int u0, int e)
+      : c(c_), sm(s_), warp(w), lane(l), u_end(e), u(u0), at(p) {
+    look();
   }
-  // move to the pair that holds unit k.u and load its page-table entry
-  __device__ __forceinline__ void seek() {
-    if (k.u >= u_end) return;
-    while (k.u >= k.s + units_of(k.len)) {
-      k.s += units_of(k.len);
-      k.len = c.len(++k.bh);
-    }
-    k.page = c.page(k.bh, (int)(k.u - k.s) * kUnit);
+  __device__ __forceinline__ void look() {
+    if (u >= u_end) return;
+    seek(c, at, u);
+    page = c.page(at.bh, (u - at.s) * kUnit);
   }
   __device__ __forceinline__ void issue() {
-    if (k.u >= u_end || dead) return;
+    if (u >= u_end || dead) return;
     const int st = put % R::kStages;
-    const bool ok = k.page >= 0 && k.page < c.n_pages;
+    const bool ok = page >= 0 && page < c.n_pages;
     good = ok ? good | (1u << st) : good & ~(1u << st);
     if (lane == 0) {
       uint64_t* bar = &sm.bar[warp][st];
       if (ok) {
-        const int r = (int)(k.u - k.s) * kUnit + k.sub * R::kRows;
-        const int64_t off = (((int64_t)k.page << c.page_log) + (r & ((1 << c.page_log) - 1))) * R::kRowBytes;
+        const int r = (u - at.s) * kUnit + sub * R::kRows;
+        const int64_t off = (((int64_t)page << c.page_log) + (r & ((1 << c.page_log) - 1))) * R::kRowBytes;
         sm100::mbar_arrive_expect_tx(bar, 2 * R::kHalf);
         sm100::bulk_load(sm.ring[warp][st][0], c.k + off, R::kHalf, bar);
         sm100::bulk_load(sm.ring[warp][st][1], c.v + off, R::kHalf, bar);
       } else {
-        c.report((uint32_t)k.page);
+        c.report((uint32_t)page);
         sm100::mbar_arrive(bar);
       }
     }
     ++put;
-    if (++k.sub == R::kSub) {
-      k.sub = 0;
-      k.u += kWarps;
-      seek();
+    if (++sub == R::kSub) {
+      sub = 0;
+      u += kWarps;
+      look();
     }
   }
   // Wait for the next stage; its number, or -1 where it holds no rows (a page
@@ -325,7 +349,7 @@ struct Bf16Rows {
   uint32_t q[kW][4];
   float o[kM][4], m[2], l[2];
 
-  __device__ __forceinline__ void start(const AttendArgs& a, int64_t b, int h, int lane) {
+  __device__ __forceinline__ void start(const AttendArgs& a, int b, int h, int lane) {
     const int gr = lane >> 2, t = lane & 3;
     const auto* qp = static_cast<const __nv_bfloat16*>(a.q) + b * a.qsb + (int64_t)(h * a.G + gr) * a.qsh;
 #pragma unroll
@@ -501,7 +525,7 @@ struct F32Rows {
     return h;
   }
 
-  __device__ __forceinline__ void start(const AttendArgs& a, int64_t b, int h, int lane) {
+  __device__ __forceinline__ void start(const AttendArgs& a, int b, int h, int lane) {
     const auto* qp = static_cast<const float*>(a.q) + b * a.qsb + (int64_t)(h * a.G) * a.qsh;
 #pragma unroll
     for (int g = 0; g < GP; ++g) {
@@ -644,30 +668,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(AttendArgs a) {
   __syncwarp();
   sm100::grid_dep_wait();
   sm100::grid_dep_launch();
-  int64_t bh, s;
-  const Cut cut = locate(a.c, a.BH, reinterpret_cast<int64_t*>(sm.merge.o), bh, s);
-  if (cut.W == 0 || blockIdx.x >= cut.g) return;
-  const int64_t u_end = cut.start(blockIdx.x + 1);
-  int64_t u = cut.start(blockIdx.x);
-  int64_t mine = u + warp;  // this warp's next unit
-  Loader<E, DH> ld(a.c, sm, warp, lane, bh, s, mine, u_end);
+  Place at;
+  bool empty;
+  const int c = blockIdx.x;
+  const Cut cut = locate(a.c, a.BH, c, reinterpret_cast<int*>(sm.merge.o), at, empty);
+  if (c >= cut.g) return;
+  const int u_end = cut.start(c + 1);
+  int u = cut.start(c);
+  int mine = u + warp;  // this warp's next unit
+  Loader<E, DH> ld(a.c, sm, warp, lane, at, mine, u_end);
   for (int i = 0; i < R::kStages; ++i) ld.issue();
   for (bool first = true; u < u_end; first = false) {
-    int len = a.c.len(bh);
-    while (len == 0) len = a.c.len(++bh);
-    const int64_t ub = units_of(len);
-    const int64_t ua = u - s, ue = min(u_end - s, ub);
+    seek(a.c, at, u);
+    const int ub = units_of(at.len);
+    const int ue = min(u_end, at.s + ub);
+    const int b = at.bh / a.H;
     Rows rows;
-    rows.start(a, bh / a.H, (int)(bh % a.H), lane);
-    for (; mine < s + ue; mine += kWarps) {
+    rows.start(a, b, at.bh - b * a.H, lane);
+    for (; mine < ue; mine += kWarps) {
 #pragma unroll
       for (int sub = 0; sub < R::kSub; ++sub) {
-        const int r = (int)(mine - s) * kUnit + sub * R::kRows;
-        const int valid = min(len - r, R::kRows);
+        const int r = (mine - at.s) * kUnit + sub * R::kRows;
+        // (a unit's second stage may lie behind the last row: valid <= 0)
+        const int valid = min(at.len - r, R::kRows);
         const int st = ld.take();
-        float* xl = a.logits ? a.logits + (bh * a.c.max_len + r) * a.G : nullptr;
+        float* xl = a.w ? a.logits + ((int64_t)at.bh * a.c.max_len + r) * a.G : nullptr;
         if (st >= 0) {
-          // (a stage of a unit's second half can lie behind the last row: valid <= 0)
           rows.step(a, sm.ring[warp][st][0], sm.ring[warp][st][1], &sm.p[warp][0][0], valid, xl, lane,
                     [&] { ld.issue(); });
         } else {
@@ -680,121 +706,132 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(AttendArgs a) {
     }
     rows.finish(sm.merge, warp, lane);
     __syncthreads();
-    finish_segment<DH>(a, sm.merge, bh, ua == 0 && ue == ub, blockIdx.x, first ? 0 : 1);
+    finish_segment<DH>(a, sm.merge, at.bh, u == at.s && ue == at.s + ub, first ? 0 : 1);
     __syncthreads();
-    u = s + ue;
-    s += ub;
-    ++bh;
+    u = ue;
   }
   ld.drain();
 }
 
-// Join the partial results of the pairs that several CTAs hold, and add the
-// weights.  CTA c takes the segments that CTA c of the first kernel took: of
-// each, its share of the pair's outputs and the weights of its own rows.
+// Join the partial results.  CTA j looks at the cut between ranges j and j + 1:
+// where it falls inside a pair, that pair has np >= 2 parts and np - 1 such
+// cuts inside, and the CTA of cut i joins share i of the pair's G d_h outputs.
+// A thread loads its parts' (m, l, o) at once and folds them; threads of the
+// same outputs fold by a tree in shared memory (a fixed order: the result does
+// not depend on timing).  One round trip to L2 after the attention's end; the
+// search for the cut runs before it.
 template <int DH>
 __global__ void __launch_bounds__(kThreads) kv_join_kernel(AttendArgs a) {
-  __shared__ float sh_f[kKvMaxGrid * kMaxG];  // factor of each part and head
-  __shared__ float sh_L[kMaxG], sh_l[kMaxG];
-  __shared__ int64_t sh_loc[kLocateWords];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int64_t bh, s;
+  __shared__ int sh_loc[kLocateWords];
+  __shared__ float2 sh_ml[kThreads];
+  __shared__ float4 sh_o[kThreads];
+  const int tid = threadIdx.x;
+  Place at;
+  bool empty;
   // the lengths were final before the first kernel passed its own wait
-  const Cut cut = locate(a.c, a.BH, sh_loc, bh, s);
+  const int c = blockIdx.x + 1;
+  const Cut cut = locate(a.c, a.BH, c, sh_loc, at, empty);
   sm100::grid_dep_wait();
-  // pairs without rows
-  for (int64_t e = blockIdx.x; e < a.BH; e += gridDim.x) {
-    if (a.c.len(e) != 0) continue;
-    const int64_t b = e / a.H;
-    const int h = (int)(e % a.H);
-    for (int i = tid; i < a.G * DH; i += kThreads)
-      a.out[b * a.osb + (int64_t)(h * a.G + i / DH) * a.osh + i % DH] = 0.f;
-    if (a.lse && tid < a.G) a.lse[e * a.G + tid] = -INFINITY;
+  sm100::grid_dep_launch();
+  if (empty) {
+    for (int e = blockIdx.x; e < a.BH; e += gridDim.x) {
+      if (a.c.len(e) != 0) continue;
+      const int b = e / a.H, h = e - b * a.H;
+      for (int i = tid * 4; i < a.G * DH; i += kThreads * 4)
+        write_out<DH>(a, e, b, h, i / DH, i % DH, -INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f));
+    }
   }
-  if (cut.W == 0 || blockIdx.x >= cut.g) return;
-  const int64_t u_end = cut.start(blockIdx.x + 1);
-  int64_t u = cut.start(blockIdx.x);
-  while (u < u_end) {
-    int len = a.c.len(bh);
-    while (len == 0) len = a.c.len(++bh);
-    const int64_t ub = units_of(len);
-    const int64_t ua = u - s, ue = min(u_end - s, ub);
-    const int64_t c0 = cut.cta_of(s), c1 = cut.cta_of(s + ub - 1);
-    const int np = (int)(c1 - c0 + 1);
-    const int stride = kv_part_floats(a.G, DH);
-    // part i is CTA c0 + i's: its first segment, but for CTA c0 where that began in an earlier pair
-    const int slot0 = cut.start(c0) == s ? 0 : 1;
-    const float* part0 = a.part + (c0 * 2 + slot0) * (int64_t)stride;
-    auto part = [&](int i) { return i == 0 ? part0 : a.part + (c0 + i) * 2 * (int64_t)stride; };
-    if (np > 1) {
-      if (warp < a.G) {
-        for (int g = warp; g < a.G; g += kWarps) {
-          float m = -INFINITY;
-          for (int i = lane; i < np; i += 32) m = fmaxf(m, part(i)[a.G * DH + g]);
-          m = warp_max(m);
-          const float mu = m == -INFINITY ? 0.f : m;
-          float l = 0.f;
-          for (int i = lane; i < np; i += 32) {
-            const float f = exp2f(part(i)[a.G * DH + g] - mu);
-            sh_f[i * kMaxG + g] = f;
-            l = fmaf(f, part(i)[a.G * DH + kMaxG + g], l);
-          }
-          l = warp_sum(l);
-          if (lane == 0) {
-            sh_l[g] = l;
-            sh_L[g] = m + log2f(l);
-          }
-        }
-      }
-      __syncthreads();
-      const int64_t b = bh / a.H;
-      const int h = (int)(bh % a.H);
-      const int j = (int)(blockIdx.x - c0), cols = a.G * DH / 4;
-      const int q0 = (int)((int64_t)cols * j / np), q1 = (int)((int64_t)cols * (j + 1) / np);
-      for (int q = q0 + warp; q < q1; q += kWarps) {
-        const int g = q / (DH / 4);
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = lane; i < np; i += 32) {
-          const float4 v = *reinterpret_cast<const float4*>(part(i) + q * 4);
-          const float f = sh_f[i * kMaxG + g];
-          o.x = fmaf(f, v.x, o.x);
-          o.y = fmaf(f, v.y, o.y);
-          o.z = fmaf(f, v.z, o.z);
-          o.w = fmaf(f, v.w, o.w);
-        }
-        o.x = warp_sum(o.x);
-        o.y = warp_sum(o.y);
-        o.z = warp_sum(o.z);
-        o.w = warp_sum(o.w);
-        if (lane == 0) {
-          const float l = sh_l[g];
-          if (l == 0.f)
-            o = make_float4(0.f, 0.f, 0.f, 0.f);
-          else
-            o = make_float4(o.x / l, o.y / l, o.z / l, o.w / l);
-          *reinterpret_cast<float4*>(a.out + b * a.osb + (int64_t)(h * a.G + g) * a.osh + (q * 4) % DH) = o;
-        }
-      }
-      if (a.lse && j == 0 && tid < a.G) a.lse[bh * a.G + tid] = kLn2 * sh_L[tid];
-    } else if (a.w) {
-      if (tid < a.G) sh_L[tid] = a.lse2[bh * a.G + tid];
-      __syncthreads();
-    }
-    if (a.w) {
-      const int r1 = min(len, (int)ue * kUnit);
-      for (int r = (int)ua * kUnit + tid; r < r1; r += kThreads) {
-        const float* x = a.logits + (bh * a.c.max_len + r) * a.G;
-        float p = 0.f;
-        for (int g = 0; g < a.G; ++g) p += sh_L[g] == -INFINITY ? 0.f : exp2f(x[g] - sh_L[g]);
-        float* w = a.w + bh * a.cap + r;
-        *w = fmaf(a.decay, *w, p);
+  if (c >= cut.g || cut.start(c) == at.s) return;
+  const int c0 = cut.range_of(at.s), np = cut.range_of(at.s + units_of(at.len) - 1) - c0 + 1;
+  const int stride = kv_part_floats(a.G, DH);
+  const int cols = a.G * DH / 4, share = c - c0 - 1;
+  const int q0 = cols * share / (np - 1), nq = cols * (share + 1) / (np - 1) - q0;
+  if (nq == 0) return;
+  int cp = 1;  // threads across the outputs; the rest of them across the parts
+  while (cp < nq && cp < kThreads) cp <<= 1;
+  const int groups = kThreads / cp, grp = tid / cp;
+  const int b = at.bh / a.H, h = at.bh - b * a.H;
+  // range c0's part of this pair is its first segment only where the range begins with the pair
+  const int slot0 = cut.start(c0) == at.s ? 0 : 1;
+  for (int qb = 0; qb < nq; qb += cp) {
+    const int q = q0 + qb + tid % cp;
+    const int g = min(q * 4 / DH, a.G - 1);
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto fold = [&](float m2, float l2, float4 o2) {
+      const float mx = fmaxf(m, m2), mu = mx == -INFINITY ? 0.f : mx;
+      const float f = exp2f(m - mu), f2 = exp2f(m2 - mu);
+      m = mx;
+      l = fmaf(l, f, l2 * f2);
+      o.x = fmaf(o.x, f, o2.x * f2);
+      o.y = fmaf(o.y, f, o2.y * f2);
+      o.z = fmaf(o.z, f, o2.z * f2);
+      o.w = fmaf(o.w, f, o2.w * f2);
+    };
+    if (q < q0 + nq) {
+#pragma unroll 4
+      for (int i = grp; i < np; i += groups) {
+        const float* part = a.part + ((c0 + i) * 2 + (i == 0 ? slot0 : 0)) * (int64_t)stride;
+        const float pm = __ldcg(part + a.G * DH + g), pl = __ldcg(part + a.G * DH + kMaxG + g);
+        fold(pm, pl, __ldcg(reinterpret_cast<const float4*>(part) + q));
       }
     }
+    sh_ml[tid] = make_float2(m, l);
+    sh_o[tid] = o;
+    for (int n = groups >> 1; n > 0; n >>= 1) {
+      __syncthreads();
+      if (grp < n) {
+        const float2 v = sh_ml[tid + n * cp];
+        fold(v.x, v.y, sh_o[tid + n * cp]);
+        sh_ml[tid] = make_float2(m, l);
+        sh_o[tid] = o;
+      }
+    }
+    if (grp == 0 && q < q0 + nq) write_out<DH>(a, at.bh, b, h, g, q * 4 % DH, m, l, o);
     __syncthreads();
-    u = s + ue;
-    s += ub;
-    ++bh;
   }
+}
+
+// w_r <- decay w_r + sum over heads of 2^(x_r - L): a CTA takes 1024 rows of a
+// pair, a thread four of them 256 rows apart.  Bound by the logits and weights
+// it reads and writes (4 G + 8 bytes a row).
+constexpr int kWeightRows = 4 * kThreads;
+
+__global__ void __launch_bounds__(kThreads) kv_weights_kernel(AttendArgs a, int chunks) {
+  const int bh = blockIdx.x / chunks, r0 = (blockIdx.x - bh * chunks) * kWeightRows + threadIdx.x;
+  const int len = a.c.len(bh);  // final before the first kernel of the call passed its wait
+  sm100::grid_dep_wait();
+  if (r0 >= len) return;
+  float L[kMaxG];
+#pragma unroll
+  for (int g = 0; g < kMaxG; ++g) L[g] = g < a.G ? __ldcg(a.lse2 + (int64_t)bh * a.G + g) : -INFINITY;
+  const float* x = a.logits + ((int64_t)bh * a.c.max_len + r0) * a.G;
+  float* w = a.w + bh * a.cap + r0;
+  float p[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    p[i] = 0.f;
+    if (r0 + i * kThreads < len)
+#pragma unroll
+      for (int g = 0; g < kMaxG; ++g)
+        if (g < a.G && L[g] != -INFINITY) p[i] += exp2f(__ldcg(x + (int64_t)i * kThreads * a.G + g) - L[g]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (r0 + i * kThreads < len) w[i * kThreads] = fmaf(a.decay, w[i * kThreads], p[i]);
+}
+
+// Let a kernel use `smem` bytes of dynamic shared memory on the current device;
+// `ready` keeps the devices (of the first 64) that have it already.
+cudaError_t allow_smem(const void* kern, size_t smem, std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 template <typename E, int DH, typename Rows>
@@ -802,15 +839,22 @@ cudaError_t launch_t(const Plan& p, const AttendArgs& a, int grid, cudaStream_t 
   auto kern = kv_attend_kernel<E, DH, Rows>;
   constexpr size_t smem = sizeof(AttendSmem<E, DH>);
   static_assert(smem <= 227 * 1024, "shared memory of one CTA");
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> ready{0};  // a bit per device: the attribute is the device's
+  cudaError_t e = allow_smem((const void*)kern, smem, ready);
   if (e != cudaSuccess) return e;
   {
     ProfScope ps(p, st, KID_KV_ATTEND);
     e = launch_pdl(kern, grid, kThreads, smem, st, a);
   }
   if (e != cudaSuccess) return e;
-  ProfScope ps(p, st, KID_KV_JOIN);
-  return launch_pdl(kv_join_kernel<DH>, grid, kThreads, 0, st, a);
+  {
+    ProfScope ps(p, st, KID_KV_JOIN);
+    e = launch_pdl(kv_join_kernel<DH>, grid, kThreads, 0, st, a);
+  }
+  if (e != cudaSuccess || !a.w) return e;
+  const int chunks = (int)ceil_div64(a.c.max_len, kWeightRows);
+  ProfScope ps(p, st, KID_KV_WEIGHTS);
+  return launch_pdl(kv_weights_kernel, (unsigned)a.BH * chunks, kThreads, 0, st, a, chunks);
 }
 
 template <int DH>
@@ -831,7 +875,7 @@ cudaError_t launch_kv_attend(const Plan& p, const KvView& c, const void* q, int6
   char* base = (char*)ws;
   AttendArgs a{};
   a.c = c;
-  a.BH = (int64_t)cfg.batch * cfg.kv_heads;
+  a.BH = cfg.batch * cfg.kv_heads;
   a.H = cfg.kv_heads;
   a.G = p.G;
   a.q = q;
@@ -847,7 +891,7 @@ cudaError_t launch_kv_attend(const Plan& p, const KvView& c, const void* q, int6
   a.scale2 = kLog2e / sqrtf((float)cfg.d_h);
   a.part = (float*)(base + L.part);
   a.lse2 = (float*)(base + L.lse2);
-  a.logits = w ? (float*)(base + L.logits) : nullptr;
+  a.logits = (float*)(base + L.logits);
   const int64_t most = a.BH * ceil_div64(c.max_len, kUnit);
   const int grid = (int)std::min<int64_t>(kKvMaxGrid, ceil_div64(most, kMinUnits));
   if (!p.bf16) return cfg.d_h == 128 ? launch_f32<128>(p, a, grid, st) : launch_f32<64>(p, a, grid, st);

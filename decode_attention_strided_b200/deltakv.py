@@ -397,16 +397,38 @@ def alloc_kv_workspace(p: Plan, max_len: int, weights: bool = False, device="cud
                        device=device)
 
 
-def _kv_tensor(name, t, dtype, shape, device):
-    """Refuse what the kernels would misread: another type, shape or layout,
-    or a tensor that does not live where the cache does."""
+_I2, _I3 = ctypes.c_int64 * 2, ctypes.c_int64 * 3
+
+
+def _kv_tensor(name, t, dtype, shape, dev):
+    """The data pointer of a contiguous tensor on CUDA device `dev` (-1: the
+    host); refuses what the kernels would misread: another type, shape, layout
+    or device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor")
-    if t.dtype is not dtype or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)}, got {t.dtype} {list(t.shape)}"
                          f"{'' if t.is_contiguous() else ' (not contiguous)'}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not with the cache")
+    return t.data_ptr()
+
+
+def _kv_meta(name, t, dtype, p, dev):
+    """A [B, H, cap] array of row weights or positions: (pointer, cap)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a tensor [{p.cfg.batch}, {p.cfg.kv_heads}, cap]")
+    cap = t.shape[2]
+    return _kv_tensor(name, t, dtype, (p.cfg.batch, p.cfg.kv_heads, cap), dev), cap
+
+
+def _kv_rows(name, t, dtype, shape, dev):
+    """The data pointer of a tensor with any strides but the last dimension's."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if t.dtype is not dtype or t.shape != shape or t.stride(-1) != 1 or t.get_device() != dev:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, contiguous in its last dimension, where the cache "
+                         f"is; got {t.dtype} {list(t.shape)}, strides {t.stride()}, on {t.device}")
     return t.data_ptr()
 
 
@@ -428,31 +450,29 @@ class KVCache:
             raise ValueError("pool must be a tensor [2, n_pages, tokens_per_page, d_h]")
         n_pages, page = int(pool.shape[1]), int(pool.shape[2])
         kv_pool_layout(p, n_pages, page, 1)
-        self.device = pool.device
-        _kv_tensor("pool", pool, c.torch_dtype(), (2, n_pages, page, c.d_h), self.device)
+        self.dev = pool.get_device()
+        pp = _kv_tensor("pool", pool, c.torch_dtype(), (2, n_pages, page, c.d_h), self.dev)
         max_pages = _page_table(p, page_table)
-        _kv_tensor("page_table", page_table, torch.int32, (c.batch, c.kv_heads, max_pages), self.device)
-        _kv_tensor("lens", lens, torch.int32, (c.batch, c.kv_heads), self.device)
+        tp = _kv_tensor("page_table", page_table, torch.int32, (c.batch, c.kv_heads, max_pages), self.dev)
+        lp = _kv_tensor("lens", lens, torch.int32, (c.batch, c.kv_heads), self.dev)
         self.plan, self.pool, self.page_table, self.lens = p, pool, page_table, lens
-        self._c = _KvCache(pool.data_ptr(), n_pages, page, page_table.data_ptr(), max_pages, lens.data_ptr(), 0)
+        self._fields = (pp, n_pages, page, tp, max_pages, lp)
 
-    def _ref(self, p, max_len, workspace):
+    def _call(self, p, max_len, workspace, stream):
+        """What every kv call passes: the C view, the workspace, its bytes and
+        the stream."""
         if self.plan is not p and self.plan.cfg != p.cfg:
             raise ValueError("the cache belongs to a plan of another configuration")
-        if self.device.type != "cuda" or self.device.index != torch.cuda.current_device():
-            raise ValueError(f"the cache is on {self.device}, not on the current CUDA device")
-        if workspace.device != self.device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
+        if self.dev < 0 or self.dev != torch.cuda.current_device():
+            raise ValueError(f"the cache is on {self.pool.device}, not on the current CUDA device")
+        if workspace.get_device() != self.dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor where the cache is")
+        if stream is None:
+            stream = torch._C._cuda_getCurrentRawStream(self.dev)
+        elif hasattr(stream, "cuda_stream"):
+            stream = stream.cuda_stream
         # a view of its own for each call: max_len belongs to the call
-        return _KvCache(self._c.pool, self._c.n_pages, self._c.tokens_per_page, self._c.page_table,
-                        self._c.max_pages, self._c.lens, max_len)
-
-
-def _kv_meta(name, t, dtype, p, device):
-    """A [B, H, cap] array of row weights or positions; (pointer, cap)."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 3:
-        raise ValueError(f"{name} must be a tensor [{p.cfg.batch}, {p.cfg.kv_heads}, cap]")
-    return _kv_tensor(name, t, dtype, (p.cfg.batch, p.cfg.kv_heads, t.shape[2]), device), int(t.shape[2])
+        return _KvCache(*self._fields, max_len), workspace.data_ptr(), workspace.nbytes, int(stream)
 
 
 def kv_append(p: Plan, cache: KVCache, max_len: int, K, V, workspace, n_tokens=None, first_pos=None, weights=None,
@@ -462,34 +482,29 @@ def kv_append(p: Plan, cache: KVCache, max_len: int, K, V, workspace, n_tokens=N
     kv-head); cache.lens already counts them.  n_tokens int32 [B]: tokens each
     sequence brings (default n_new).  pos int32 and weights float32 [B, H, cap]
     get first_pos[b] + t and token_weights [B, H, n_new] (0 where None)."""
-    c, B, H = p.cfg, p.cfg.batch, p.cfg.kv_heads
-    dev = cache.device
-    if K.dim() != 4 or V.shape != K.shape or tuple(K.shape[:2]) != (B, H) or K.shape[3] != c.d_h:
-        raise ValueError(f"K and V must have shape [{B}, {H}, n_new, {c.d_h}], got {list(K.shape)}, {list(V.shape)}")
-    if K.dtype is not c.torch_dtype() or V.dtype is not c.torch_dtype() or K.device != dev or V.device != dev:
-        raise ValueError(f"K and V must be {c.torch_dtype()} on {dev}")
-    n_new = int(K.shape[2])
+    c, dev = p.cfg, cache.dev
+    B, H = c.batch, c.kv_heads
+    if not isinstance(K, torch.Tensor) or K.dim() != 4:
+        raise ValueError(f"K and V must have shape [{B}, {H}, n_new, {c.d_h}]")
+    n_new = K.shape[2]
+    shape, dt = (B, H, n_new, c.d_h), c.torch_dtype()
+    kp, vp = _kv_rows("K", K, dt, shape, dev), _kv_rows("V", V, dt, shape, dev)
     if n_new == 0:
         return
-    if K.stride(3) != 1 or V.stride(3) != 1:
-        raise ValueError("K and V must be contiguous in their last dimension")
-    if any(a != b for a, b, n in zip(K.stride(), V.stride(), K.shape) if n > 1):
+    ks = (_stride(K, 0), _stride(K, 1), _stride(K, 2, c.d_h))
+    if ks != (_stride(V, 0), _stride(V, 1), _stride(V, 2, c.d_h)):
         raise ValueError("K and V must share strides")
     nt = None if n_tokens is None else _kv_tensor("n_tokens", n_tokens, torch.int32, (B,), dev)
     fp = None if first_pos is None else _kv_tensor("first_pos", first_pos, torch.int32, (B,), dev)
-    tw = None if token_weights is None else _kv_tensor("token_weights", token_weights, torch.float32, (B, H, n_new), dev)
-    w = pp = None
-    cap = cap_p = 0
-    if weights is not None:
-        w, cap = _kv_meta("weights", weights, torch.float32, p, dev)
-    if pos is not None:
-        pp, cap_p = _kv_meta("pos", pos, torch.int32, p, dev)
-    if w is not None and pp is not None and cap != cap_p:
+    tw = None if token_weights is None else _kv_tensor("token_weights", token_weights, torch.float32, (B, H, n_new),
+                                                       dev)
+    w, cap = (None, 0) if weights is None else _kv_meta("weights", weights, torch.float32, p, dev)
+    pp, cap_p = (None, cap) if pos is None else _kv_meta("pos", pos, torch.int32, p, dev)
+    if w is not None and cap != cap_p:
         raise ValueError(f"weights and pos must have the same cap, got {cap} and {cap_p}")
-    _check("deltakv_kv_append", load_library().deltakv_kv_append(
-        p.handle, cache._ref(p, int(max_len), workspace), n_new, K.data_ptr(), V.data_ptr(),
-        (ctypes.c_int64 * 3)(_stride(K, 0), _stride(K, 1), _stride(K, 2, c.d_h)), nt, fp, w, pp, max(cap, cap_p), tw, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+    view, ws, nbytes, st = cache._call(p, max_len, workspace, stream)
+    _check("deltakv_kv_append", _lib.deltakv_kv_append(
+        p.handle, view, n_new, kp, vp, _I3(*ks), nt, fp, w, pp, cap_p, tw, ws, nbytes, st))
 
 
 def kv_decode_attention(p: Plan, cache: KVCache, max_len: int, q, out, workspace, weights=None, decay: float = 1.0,
@@ -497,19 +512,16 @@ def kv_decode_attention(p: Plan, cache: KVCache, max_len: int, q, out, workspace
     """deltakv_kv_decode_attention: q [B, Hq, d_h] -> out [B, Hq, d_h]
     float32, lse float32 [B, Hq]; weights float32 [B, H, cap] gather each
     row's attention weight (decay w + p)."""
-    c, dev = p.cfg, cache.device
+    c, dev = p.cfg, cache.dev
     shape = (c.batch, c.q_heads, c.d_h)
-    if tuple(q.shape) != shape or q.dtype is not c.torch_dtype() or q.stride(2) != 1 or q.device != dev:
-        raise ValueError(f"q must be {c.torch_dtype()} {list(shape)} on {dev}, contiguous in its last dimension")
-    if tuple(out.shape) != shape or out.dtype is not torch.float32 or out.stride(2) != 1 or out.device != dev:
-        raise ValueError(f"out must be float32 {list(shape)} on {dev}, contiguous in its last dimension")
+    qp = _kv_rows("q", q, c.torch_dtype(), shape, dev)
+    op = _kv_rows("out", out, torch.float32, shape, dev)
     w, cap = (None, 0) if weights is None else _kv_meta("weights", weights, torch.float32, p, dev)
-    ls = None if lse is None else _kv_tensor("lse", lse, torch.float32, shape[:2], dev)
-    _check("deltakv_kv_decode_attention", load_library().deltakv_kv_decode_attention(
-        p.handle, cache._ref(p, int(max_len), workspace), q.data_ptr(),
-        (ctypes.c_int64 * 2)(_stride(q, 0), _stride(q, 1)), out.data_ptr(),
-        (ctypes.c_int64 * 2)(_stride(out, 0), _stride(out, 1)), ls, w, cap, float(decay), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+    lp = None if lse is None else _kv_tensor("lse", lse, torch.float32, shape[:2], dev)
+    view, ws, nbytes, st = cache._call(p, max_len, workspace, stream)
+    _check("deltakv_kv_decode_attention", _lib.deltakv_kv_decode_attention(
+        p.handle, view, qp, _I2(_stride(q, 0), _stride(q, 1)), op, _I2(_stride(out, 0), _stride(out, 1)), lp, w, cap,
+        decay, ws, nbytes, st))
 
 
 def kv_evict(p: Plan, cache: KVCache, max_len: int, budget, weights, pos, workspace, n_first: int = 0,
@@ -518,20 +530,18 @@ def kv_evict(p: Plan, cache: KVCache, max_len: int, budget, weights, pos, worksp
     kv-head), those of the first n_first and last n_recent positions and then
     the largest weights.  lens_out, weights_out and pos_out default to
     cache.lens, weights and pos (in place)."""
-    B, H, dev = p.cfg.batch, p.cfg.kv_heads, cache.device
-    lens_out = cache.lens if lens_out is None else lens_out
-    weights_out = weights if weights_out is None else weights_out
-    pos_out = pos if pos_out is None else pos_out
+    dev = cache.dev
+    pairs = (p.cfg.batch, p.cfg.kv_heads)
     w, cap = _kv_meta("weights", weights, torch.float32, p, dev)
-    shape = (B, H, cap)
-    ptrs = [_kv_tensor("pos", pos, torch.int32, shape, dev),
-            _kv_tensor("weights_out", weights_out, torch.float32, shape, dev),
-            _kv_tensor("pos_out", pos_out, torch.int32, shape, dev)]
-    _check("deltakv_kv_evict", load_library().deltakv_kv_evict(
-        p.handle, cache._ref(p, int(max_len), workspace),
-        _kv_tensor("budget", budget, torch.int32, (B, H), dev), int(n_first), int(n_recent), w, *ptrs, cap,
-        _kv_tensor("lens_out", lens_out, torch.int32, (B, H), dev), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+    shape = (*pairs, cap)
+    pp = _kv_tensor("pos", pos, torch.int32, shape, dev)
+    wo = w if weights_out is None else _kv_tensor("weights_out", weights_out, torch.float32, shape, dev)
+    po = pp if pos_out is None else _kv_tensor("pos_out", pos_out, torch.int32, shape, dev)
+    bp = _kv_tensor("budget", budget, torch.int32, pairs, dev)
+    lo = _kv_tensor("lens_out", cache.lens if lens_out is None else lens_out, torch.int32, pairs, dev)
+    view, ws, nbytes, st = cache._call(p, max_len, workspace, stream)
+    _check("deltakv_kv_evict", _lib.deltakv_kv_evict(
+        p.handle, view, bp, n_first, n_recent, w, pp, wo, po, cap, lo, ws, nbytes, st))
 
 
 def reconstruct(p: Plan, T: int, cache, W3, b3, W4, b4, K_out, V_out, workspace, stream=None):
