@@ -8,7 +8,7 @@
 // A part of the rows gives (m, l, o = sum 2^(x_r - m) V_r); parts join by
 // m = max m_i, l = sum 2^(m_i - m) l_i, o = sum 2^(m_i - m) o_i.
 //
-// Split: all pairs' rows, in units of 16, form one list that is cut into as
+// Split: all pairs' rows, in units of 16 to 64 (8 KB of K), form one list that is cut into as
 // many equal ranges as there are CTAs, so that lengths do not matter for the
 // balance.  A CTA's range is a run of segments, each inside one pair; only
 // its first and its last segment can be a part of a pair, so a CTA leaves two
@@ -27,14 +27,20 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnit = 16;       // rows per unit of the split (divides every page)
-constexpr int kMinUnits = 8;    // a CTA gets at least these, or fewer CTAs work
+constexpr int kGroup = 16;         // rows of the smallest page
+constexpr int kSlotBytes = 8192;   // K or V rows of one unit of the split
+constexpr int kSlots = 3;          // of a warp's ring
+constexpr int kMinUnits = 4;       // a CTA gets at least these, or fewer CTAs work
+// rows per unit
+template <typename E, int DH>
+constexpr int kUnitRows = kSlotBytes / (DH * (int)sizeof(E));
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct AttendArgs {
   KvView c;
   int BH, H, G;
+  int unit_log;   // log2 of the rows per unit
   const void* q;
   int64_t qsb, qsh;
   float* out;
@@ -66,14 +72,17 @@ struct Place {
   int bh, s, len;
 };
 
-__device__ __forceinline__ int units_of(int len) { return (len + kUnit - 1) / kUnit; }
+// units of len rows
+__device__ __forceinline__ int units_of(int len, int unit_log) { return (len + (1 << unit_log) - 1) >> unit_log; }
 
 // The cut, and the pair that holds the first unit of range c, by a block scan
 // over the lengths.  Every thread returns the same values; sh: kLocateWords
 // of shared memory, free again on return.  Lengths out of range are reported
 // here; `empty` tells whether any pair holds no row.
 constexpr int kLocateWords = kWarps + 4;
-__device__ __forceinline__ Cut locate(const KvView& k, int BH, int c, int* sh, Place& at, bool& empty) {
+__device__ __forceinline__ Cut locate(const AttendArgs& a, int c, int* sh, Place& at, bool& empty) {
+  const KvView& k = a.c;
+  const int BH = a.BH;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (BH + kThreads - 1) / kThreads;
   const int b0 = min(BH, tid * per), b1 = min(BH, b0 + per);
@@ -83,7 +92,7 @@ __device__ __forceinline__ Cut locate(const KvView& k, int BH, int c, int* sh, P
     last = k.checked(raw);
     if (raw != last) k.report((uint32_t)raw);
     none |= last == 0;
-    sum += units_of(last);
+    sum += units_of(last, a.unit_log);
   }
   int inc = sum;
 #pragma unroll
@@ -91,7 +100,7 @@ __device__ __forceinline__ Cut locate(const KvView& k, int BH, int c, int* sh, P
     const int v = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += v;
   }
-  if (lane == 31) sh[warp] = inc;
+  if (lane == 31 && warp < kWarps) sh[warp] = inc;
   empty = __syncthreads_or(none) != 0;
   int before = 0, W = 0;
 #pragma unroll
@@ -112,8 +121,8 @@ __device__ __forceinline__ Cut locate(const KvView& k, int BH, int c, int* sh, P
       if (per > 1)
         for (;; ++b) {
           last = k.len(b);
-          if (target < s + units_of(last)) break;
-          s += units_of(last);
+          if (target < s + units_of(last, a.unit_log)) break;
+          s += units_of(last, a.unit_log);
         }
       sh[kWarps] = b;
       sh[kWarps + 1] = s;
@@ -126,13 +135,26 @@ __device__ __forceinline__ Cut locate(const KvView& k, int BH, int c, int* sh, P
   return cut;
 }
 
-// Move to the pair that holds unit u (at or after the present one).
-__device__ __forceinline__ void seek(const KvView& k, Place& at, int u) {
-  while (u >= at.s + units_of(at.len)) {
-    at.s += units_of(at.len);
-    at.len = k.len(++at.bh);
+// The lengths of the pairs from bh0 on, the first kLensTable of them in shared
+// memory: a CTA with many short pairs steps through them without a trip to L2
+// for each.
+constexpr int kLensTable = 256;
+struct Lens {
+  const KvView& k;
+  const int* table;
+  int bh0, unit_log;
+  __device__ __forceinline__ int operator()(int bh) const {
+    const int i = bh - bh0;
+    return i < kLensTable ? table[i] : k.len(bh);
   }
-}
+  // move to the pair that holds unit u (at or after the present one)
+  __device__ __forceinline__ void seek(Place& at, int u) const {
+    while (u >= at.s + units_of(at.len, unit_log)) {
+      at.s += units_of(at.len, unit_log);
+      at.len = (*this)(++at.bh);
+    }
+  }
+};
 
 // One warp's running softmax over its rows, as partial results: m, l and o
 // per head, reduced over the block's warps in shared memory.
@@ -193,101 +215,132 @@ __device__ __forceinline__ void finish_segment(const AttendArgs& a, const Merge<
   }
 }
 
-// ---- the tiles of one warp
-// A warp takes every eighth unit of its CTA's range and streams its rows
-// through a ring of shared-memory stages of its own: lane 0 issues one bulk
-// copy of a stage's K rows and one of its V rows (rows of a page are
-// contiguous, and a stage never leaves its page), an mbarrier per stage tells
-// when they have landed, and the stage is refilled as soon as its rows are in
-// registers.  No other warp takes part, so the warps drift freely between the
-// segments' ends.
-template <typename E, int DH>
-struct Ring {
-  static constexpr int kRowBytes = DH * (int)sizeof(E);
-  static constexpr int kRows = kRowBytes == 512 ? 8 : 16;       // rows per stage
-  static constexpr int kSub = kUnit / kRows;                    // stages per unit
-  static constexpr int kHalf = kRows * kRowBytes;               // bytes of K (or V) per stage
-  static constexpr int kStages = 24 * 1024 / (2 * kHalf);       // 3 stages of 8 KB, or 6 of 4 KB
-};
-
+// ---- the rows' way into shared memory
+// A warp takes every eighth unit of its CTA's range through a ring of three
+// 8 KB slots of its own, K rows and V rows in turn: lane 0 issues bulk copies
+// (one per slot where a page holds a unit, else one per page), a barrier per
+// slot tells when they have landed, and a slot is refilled as soon as its rows
+// are in registers.  No other warp takes part, so the warps drift freely
+// between the segments' ends.  Plain copies in this pattern reach 7.3 TB/s with
+// 8 KB copies and 96 to 128 KB in flight per SM, 6.6 with 4 KB copies and 192
+// KB, 5.3 with 2 KB copies.
 template <typename E, int DH>
 struct AttendSmem {
-  alignas(128) char ring[kWarps][Ring<E, DH>::kStages][2][Ring<E, DH>::kHalf];
+  alignas(128) char ring[kWarps][kSlots][kSlotBytes];
   Merge<DH> merge;
-  // float32 rows: the weights of a stage's rows, then the rescaling factors
-  float p[kWarps][sizeof(E) == 4 ? Ring<E, DH>::kRows + 1 : 1][kMaxG];
-  uint64_t bar[kWarps][Ring<E, DH>::kStages];
+  int lens[kLensTable];
+  uint64_t bar[kWarps][kSlots];
+  int dead;  // a wait ran out: nothing more is issued or waited for
 };
 
 template <typename E, int DH>
 struct Loader {
-  using R = Ring<E, DH>;
-  const KvView& c;
+  static constexpr int kRows = kUnitRows<E, DH>;
+  static constexpr int kGroups = kRows / kGroup;  // 1, 2 or 4
+  static constexpr int kRowBytes = DH * (int)sizeof(E);
+  static constexpr int kBatch = 32 / kGroups;     // units looked up at a time
+  const Lens& lens;
   AttendSmem<E, DH>& sm;
   const int warp, lane, u_end;
-  // the next stage's unit, its pair, its part of the unit and its page-table
-  // entry (loaded one unit ahead); all lanes hold the same values
-  int u, sub = 0;
+  // The warp's units kBatch at a time: lane i looks up group i % kGroups of the
+  // (i / kGroups)-th of them (its pair, then its page), all at once; off: the
+  // byte offset of the group's rows in both planes, or -1 where the page is out
+  // of range or the group lies behind the last row.
+  int u0, nth = 0;
   Place at;
-  int32_t page;
-  int put = 0, get = 0;   // stages issued and taken
-  uint32_t good = 0;      // bit i: stage i's page is in range
-  bool dead = false;      // a wait ran out: nothing more is issued
+  int64_t off = -1;
+  int rows = 0;            // valid rows of the lane's group
+  int put = 0, slot = 0;   // copies issued: `put` K and V slots; next slot to fill
+  int get = 0, gslot = 0, parity = 0;
+  uint32_t good = 0;       // bit k of units issued last in the high bits: group k's rows are there
+  bool dead = false;
 
-  __device__ Loader(const KvView& c_, AttendSmem<E, DH>& s_, int w, int l, Place p, int u0, int e)
-      : c(c_), sm(s_), warp(w), lane(l), u_end(e), u(u0), at(p) {
+  __device__ __forceinline__ Loader(const Lens& l_, AttendSmem<E, DH>& s_, int w, int l, Place p, int u, int e)
+      : lens(l_), sm(s_), warp(w), lane(l), u_end(e), u0(u), at(p) {
     look();
   }
   __device__ __forceinline__ void look() {
+    const KvView& c = lens.k;
+    const int u = u0 + lane / kGroups * kWarps;
+    off = -1;
+    rows = 0;
     if (u >= u_end) return;
-    seek(c, at, u);
-    page = c.page(at.bh, (u - at.s) * kUnit);
+    lens.seek(at, u);
+    const int r = (u - at.s) * kRows + lane % kGroups * kGroup;
+    if (r >= at.len) return;
+    rows = min(at.len - r, kGroup);
+    const int32_t page = c.page(at.bh, r);
+    if (page < 0 || page >= c.n_pages)
+      c.report((uint32_t)page);
+    else
+      off = (((int64_t)page << c.page_log) + (r & ((1 << c.page_log) - 1))) * kRowBytes;
   }
+  // Issue the next slot's copies: K rows of a unit, then its V rows.
   __device__ __forceinline__ void issue() {
-    if (u >= u_end || dead) return;
-    const int st = put % R::kStages;
-    const bool ok = page >= 0 && page < c.n_pages;
-    good = ok ? good | (1u << st) : good & ~(1u << st);
+    if (u0 + nth * kWarps >= u_end || dead) return;
+    const KvView& c = lens.k;
+    const bool is_v = put & 1;
+    char* dst = sm.ring[warp][slot];
+    uint64_t* bar = &sm.bar[warp][slot];
+    const char* plane = is_v ? c.v : c.k;
+    const uint32_t have = __ballot_sync(0xffffffffu, off >= 0) >> (nth * kGroups) & ((1u << kGroups) - 1);
+    if (!is_v) good = good << kGroups | have;
+    const int total = __reduce_add_sync(0xffffffffu, lane / kGroups == nth && off >= 0 ? rows : 0) * kRowBytes;
+    // lane 0 has the whole unit where one page does; else each group's lane copies its own
+    const bool one = kGroups == 1 || c.page_log >= 4 + (kGroups == 2 ? 1 : 2);
+    const int64_t o = one ? __shfl_sync(0xffffffffu, off, nth * kGroups) : off;
     if (lane == 0) {
-      uint64_t* bar = &sm.bar[warp][st];
-      if (ok) {
-        const int r = (u - at.s) * kUnit + sub * R::kRows;
-        const int64_t off = (((int64_t)page << c.page_log) + (r & ((1 << c.page_log) - 1))) * R::kRowBytes;
-        sm100::mbar_arrive_expect_tx(bar, 2 * R::kHalf);
-        sm100::bulk_load(sm.ring[warp][st][0], c.k + off, R::kHalf, bar);
-        sm100::bulk_load(sm.ring[warp][st][1], c.v + off, R::kHalf, bar);
-      } else {
-        c.report((uint32_t)page);
+      if (total)
+        sm100::mbar_arrive_expect_tx(bar, total);
+      else
         sm100::mbar_arrive(bar);
-      }
+      if (one && total) sm100::bulk_load(dst, plane + o, total, bar);
+    }
+    if (!one) {
+      __syncwarp();
+      if (lane / kGroups == nth && off >= 0)
+        sm100::bulk_load(dst + lane % kGroups * kGroup * kRowBytes, plane + o, rows * kRowBytes, bar);
     }
     ++put;
-    if (++sub == R::kSub) {
-      sub = 0;
-      u += kWarps;
+    if (++slot == kSlots) slot = 0;
+    if (is_v && ++nth == kBatch) {
+      nth = 0;
+      u0 += kBatch * kWarps;
       look();
+      __syncwarp();
     }
   }
-  // Wait for the next stage; its number, or -1 where it holds no rows (a page
-  // out of range, or a wait that ran out).
-  __device__ __forceinline__ int take() {
-    const int st = get % R::kStages;
+  // Wait for the next slot; null where a wait ran out.
+  __device__ __forceinline__ char* take() {
     if (!dead) {
-      const bool got = sm100::mbar_wait_drain(&sm.bar[warp][st], (get / R::kStages) & 1);
+      const bool got = sm100::mbar_wait(&sm.bar[warp][gslot], parity, &sm.dead);
       if (__any_sync(0xffffffffu, !got)) {
         dead = true;
-        if (lane == 0) latch_error(c.err, DELTAKV_ERR_DEVICE_TIMEOUT, 0u);
+        if (lane == 0) {
+          *(volatile int*)&sm.dead = 1;
+          latch_error(lens.k.err, DELTAKV_ERR_DEVICE_TIMEOUT, 0u);
+        }
       }
     }
-    if (dead) return -1;
+    if (dead) return nullptr;
+    char* p = sm.ring[warp][gslot];
     ++get;
-    return good >> st & 1 ? st : -1;
+    if (++gslot == kSlots) {
+      gslot = 0;
+      parity ^= 1;
+    }
+    return p;
   }
-  // on the way out after a wait ran out: no copy may land in shared memory
-  // that the CTA no longer owns
+  // Groups of the unit whose K slot was taken last that hold rows.
+  __device__ __forceinline__ uint32_t groups() const {
+    // units whose K was issued after it: (K slots issued) - (K slots taken)
+    const int later = (put + 1) / 2 - (get + 1) / 2;
+    return good >> (later * kGroups) & ((1u << kGroups) - 1);
+  }
+  // on the way out after a wait ran out: no copy may land in shared memory that the CTA no longer owns
   __device__ void drain() {
     if (dead)
-      for (int i = get; i < put; ++i) sm100::mbar_wait_drain(&sm.bar[warp][i % R::kStages], (i / R::kStages) & 1);
+      for (int i = get; i < put; ++i) sm100::mbar_wait_drain(&sm.bar[warp][i % kSlots], (i / kSlots) & 1);
   }
 };
 
@@ -324,10 +377,10 @@ __device__ __forceinline__ uint32_t finite_halves(uint32_t v) {
   return v & ~((t >> 15 & 0x00010001u) * 0xffffu);
 }
 
-// bfloat16 rows on the tensor cores, 16 rows a step.  Lane (gr, t) = (lane /
-// 4, lane % 4).  Rows are the M side of both products and the pair's query
-// heads (at most 8, zero beyond G) the N side, so no product is wasted on
-// padding: X[row][head] = K Q^T, and O[dim][head] += V^T P.
+// bfloat16 rows on the tensor cores, a unit (32 or 64 rows) a step, in groups
+// of 16.  Lane (gr, t) = (lane / 4, lane % 4).  Rows are the M side of both
+// products and the pair's query heads (at most 8, zero beyond G) the N side, so
+// no product is wasted on padding: X[row][head] = K Q^T, O[dim][head] += V^T P.
 //  - X: the contraction index is permuted so that a lane's four 32-bit
 //    operands of two k-steps are one 16-byte word of its K row (the same word
 //    of the query row), read straight from the row.
@@ -335,23 +388,27 @@ __device__ __forceinline__ uint32_t finite_halves(uint32_t v) {
 //    2t+8, 2t+9 hold its operands once the two rows of a pair are interleaved
 //    (byte permutes); P comes out of X's accumulators by an 8x8 transpose.
 //  - P in three bfloat16 terms (24 bits of it): with one, each weight would
-//    carry 2^-8 into a float32 result.  The extra products cost nothing here:
-//    the tensor pipe is far from full.  An infinite V element must meet the
-//    first term only (the others may be zero or negative), so the others take
-//    V with such elements zeroed where a step has any.
+//    carry 2^-8 into a float32 result.  The extra products cost little: the
+//    tensor pipe is far from full.  An infinite V element must meet the first
+//    term only (the others may be zero or negative), so the others take V with
+//    such elements zeroed where a step has any.
 //  - A step's products go into zeroed accumulators that are then added to the
 //    running ones in float32: the tensor core's own additions may truncate,
 //    which over thousands of steps would bias the sums.
 template <int DH>
 struct Bf16Rows {
-  static constexpr int kW = DH / 32;       // 16-byte words of a row per lane and product (K), of DH / 8 in all
+  using E = __nv_bfloat16;
+  static constexpr int kG = kUnitRows<E, DH> / kGroup;
+  static constexpr int kW = DH / 32;       // 16-byte words of a K row per lane
   static constexpr int kM = DH / 16;       // M tiles of O
+  static constexpr int kH = DH / 64;       // 16-byte words of a V row per lane
   uint32_t q[kW][4];
   float o[kM][4], m[2], l[2];
 
-  __device__ __forceinline__ void start(const AttendArgs& a, int b, int h, int lane) {
+  __device__ __forceinline__ void start(const AttendArgs& a, int bh, int lane) {
+    const int b = bh / a.H, h = bh - b * a.H;
     const int gr = lane >> 2, t = lane & 3;
-    const auto* qp = static_cast<const __nv_bfloat16*>(a.q) + b * a.qsb + (int64_t)(h * a.G + gr) * a.qsh;
+    const auto* qp = static_cast<const E*>(a.q) + b * a.qsb + (int64_t)(h * a.G + gr) * a.qsh;
 #pragma unroll
     for (int i = 0; i < kW; ++i) {
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -367,111 +424,154 @@ struct Bf16Rows {
     l[0] = l[1] = 0.f;
   }
 
-  // Rows [r, r + 16) of the pair, of which `valid` count; xl: their logits in
-  // global memory, or null.  `refill` is called once the rows are in registers.
-  template <typename F>
-  __device__ __forceinline__ void step(const AttendArgs& a, const char* ks, const char* vs, float* p_smem, int valid,
-                                       float* xl, int lane, F refill) {
+  // The unit `in` holds next: `valid` rows (at least one) from row r on; xl:
+  // their logits in global memory, or null.
+  __device__ __forceinline__ void step(const AttendArgs& a, Loader<E, DH>& in, int valid, float* xl, int lane) {
     const int gr = lane >> 2, t = lane & 3;
-    float x0[4] = {0.f, 0.f, 0.f, 0.f}, x1[4] = {0.f, 0.f, 0.f, 0.f};
+    const char* ks = in.take();
+    if (!ks) return;
+    const uint32_t have = in.groups();
+    float x[kG][4];
 #pragma unroll
-    for (int i = 0; i < kW; ++i) {
-      const uint4 ka = *reinterpret_cast<const uint4*>(ks + gr * DH * 2 + (i * 4 + t) * 16);
-      const uint4 kb = *reinterpret_cast<const uint4*>(ks + (gr + 8) * DH * 2 + (i * 4 + t) * 16);
-      mma_bf16(x0, ka.x, kb.x, ka.y, kb.y, q[i][0], q[i][1]);
-      mma_bf16(x1, ka.z, kb.z, ka.w, kb.w, q[i][2], q[i][3]);
-    }
-    // V rows 2t, 2t + 1, 2t + 8, 2t + 9: words gr (and gr + 8)
-    constexpr int kH = DH / 64;
-    uint4 v[kH][4];
+    for (int n = 0; n < kG; ++n) {
+      float x0[4] = {0.f, 0.f, 0.f, 0.f}, x1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = 2 * t + (i & 1) + (i >> 1) * 8;
+      for (int i = 0; i < kW; ++i) {
+        const uint4 ka = *reinterpret_cast<const uint4*>(ks + (n * kGroup + gr) * DH * 2 + (i * 4 + t) * 16);
+        const uint4 kb = *reinterpret_cast<const uint4*>(ks + (n * kGroup + gr + 8) * DH * 2 + (i * 4 + t) * 16);
+        mma_bf16(x0, ka.x, kb.x, ka.y, kb.y, q[i][0], q[i][1]);
+        mma_bf16(x1, ka.z, kb.z, ka.w, kb.w, q[i][2], q[i][3]);
+      }
 #pragma unroll
-      for (int w = 0; w < kH; ++w) v[w][i] = *reinterpret_cast<const uint4*>(vs + row * DH * 2 + (w * 8 + gr) * 16);
+      for (int i = 0; i < 4; ++i) x[n][i] = (x0[i] + x1[i]) * a.scale2;
     }
     __syncwarp();
-    refill();
-    float x[4];
+    in.issue();
+    const bool full = valid == kG * kGroup && have == (1u << kG) - 1;
+    if (!full) {
+      // rows that do not count: whatever the slot holds
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = (x0[i] + x1[i]) * a.scale2;
-    if (valid < kUnit) {
-      // rows behind the last: whatever the page holds must not count (0 x NaN)
-      if (gr >= valid) x[0] = x[1] = -INFINITY;
-      if (gr + 8 >= valid) x[2] = x[3] = -INFINITY;
+      for (int n = 0; n < kG; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (2 * t + (i & 1) + (i >> 1) * 8 >= valid)
-#pragma unroll
-          for (int w = 0; w < kH; ++w) v[w][i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < 4; ++i)
+          if (n * kGroup + gr + (i >> 1) * 8 >= valid || !(have >> n & 1)) x[n][i] = -INFINITY;
     }
     if (xl) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = gr + (i >> 1) * 8, g = 2 * t + (i & 1);
-        if (row < valid && g < a.G) xl[(int64_t)row * a.G + g] = x[i];
-      }
+      for (int n = 0; n < kG; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = n * kGroup + gr + (i >> 1) * 8, g = 2 * t + (i & 1);
+          if (row < valid && g < a.G) xl[(int64_t)row * a.G + g] = x[n][i];
+        }
     }
-    float f[2], p[4];
+    float f[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      float mx = fmaxf(x[c], x[c + 2]);
+      float mx = m[c];
+#pragma unroll
+      for (int n = 0; n < kG; ++n) mx = fmaxf(mx, fmaxf(x[n][c], x[n][c + 2]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-      mx = fmaxf(mx, m[c]);
       const float mu = mx == -INFINITY ? 0.f : mx;
       f[c] = exp2f(m[c] - mu);
       m[c] = mx;
-      p[c] = exp2f(x[c] - mu);
-      p[c + 2] = exp2f(x[c + 2] - mu);
-      l[c] = fmaf(l[c], f[c], p[c] + p[c + 2]);
+      l[c] *= f[c];
+#pragma unroll
+      for (int n = 0; n < kG; ++n) {
+        x[n][c] = exp2f(x[n][c] - mu);
+        x[n][c + 2] = exp2f(x[n][c + 2] - mu);
+        l[c] += x[n][c] + x[n][c + 2];
+      }
     }
-    uint32_t nz[4] = {0u, 0u, 0u, 0u};
+    uint32_t pb[kG][3][2];
 #pragma unroll
-    for (int w = 0; w < kH; ++w)
+    for (int n = 0; n < kG; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        note_nonfinite(nz[0], v[w][i].x);
-        note_nonfinite(nz[1], v[w][i].y);
-        note_nonfinite(nz[2], v[w][i].z);
-        note_nonfinite(nz[3], v[w][i].w);
-      }
-    // the halves are zero or NaN
-    const bool odd = __any_sync(0xffffffffu, ((nz[0] | nz[1] | nz[2] | nz[3]) & 0x7fff7fffu) != 0u);
-    uint32_t pb[3][2];
+      for (int s = 0; s < 3; ++s)
 #pragma unroll
-    for (int s = 0; s < 3; ++s)
+        for (int hf = 0; hf < 2; ++hf) {
+          const uint32_t w = pack_bf16(x[n][2 * hf], x[n][2 * hf + 1]);
+          x[n][2 * hf] -= lo_f(w);
+          x[n][2 * hf + 1] -= hi_f(w);
+          pb[n][s][hf] = transpose8(w);
+        }
+    const char* vs = in.take();
+    if (!vs) return;
+    float c[kM][4];
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const uint32_t w = pack_bf16(p[2 * hf], p[2 * hf + 1]);
-        p[2 * hf] -= lo_f(w);
-        p[2 * hf + 1] -= hi_f(w);
-        pb[s][hf] = transpose8(w);
-      }
+    for (int j = 0; j < kM; ++j) c[j][0] = c[j][1] = c[j][2] = c[j][3] = 0.f;
 #pragma unroll
-    for (int j = 0; j < kM; ++j) {
-      // M rows gr and gr + 8 of tile j: dims 8 gr + j and 64 + 8 gr + j (DH 128), 8 gr + 2 j and 8 gr + 2 j + 1 (64)
-      uint32_t av[4];
+    for (int n = 0; n < kG; ++n) {
+      // V rows 2t, 2t + 1, 2t + 8, 2t + 9 of the group: words gr (and gr + 8)
+      uint4 v[kH][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int up = i & 1, pr = i >> 1;  // a0: rows gr, tokens 2t..; a1: rows gr + 8; a2, a3: tokens 2t + 8..
-        const uint32_t* ra = reinterpret_cast<const uint32_t*>(&v[kH == 2 ? up : 0][2 * pr]);
-        const uint32_t* rb = reinterpret_cast<const uint32_t*>(&v[kH == 2 ? up : 0][2 * pr + 1]);
-        const int word = kH == 2 ? j >> 1 : j;
-        const bool high = kH == 2 ? j & 1 : up;
-        av[i] = __byte_perm(ra[word], rb[word], high ? 0x7632 : 0x5410);
+        const int row = n * kGroup + 2 * t + (i & 1) + (i >> 1) * 8;
+#pragma unroll
+        for (int w = 0; w < kH; ++w) {
+          v[w][i] = *reinterpret_cast<const uint4*>(vs + row * DH * 2 + (w * 8 + gr) * 16);
+          if (!full && (row >= valid || !(have >> n & 1))) v[w][i] = make_uint4(0u, 0u, 0u, 0u);
+        }
       }
-      uint32_t lv[4] = {av[0], av[1], av[2], av[3]};
-      if (odd)
+      if (n == kG - 1) {
+        __syncwarp();
+        in.issue();
+      }
+      uint32_t nz[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) lv[i] = finite_halves(lv[i]);
-      float c[4] = {0.f, 0.f, 0.f, 0.f};
-      mma_bf16(c, lv[0], lv[1], lv[2], lv[3], pb[2][0], pb[2][1]);
-      mma_bf16(c, lv[0], lv[1], lv[2], lv[3], pb[1][0], pb[1][1]);
-      mma_bf16(c, av[0], av[1], av[2], av[3], pb[0][0], pb[0][1]);
+      for (int w = 0; w < kH; ++w)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[j][i] = fmaf(o[j][i], f[i & 1], c[i]);
+        for (int i = 0; i < 4; ++i) {
+          note_nonfinite(nz[0], v[w][i].x);
+          note_nonfinite(nz[1], v[w][i].y);
+          note_nonfinite(nz[2], v[w][i].z);
+          note_nonfinite(nz[3], v[w][i].w);
+        }
+      // the halves are zero or NaN
+      if (!__any_sync(0xffffffffu, ((nz[0] | nz[1] | nz[2] | nz[3]) & 0x7fff7fffu) != 0u))
+        outputs<false>(c, v, pb[n]);
+      else
+        outputs<true>(c, v, pb[n]);
+    }
+#pragma unroll
+    for (int j = 0; j < kM; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[j][i] = fmaf(o[j][i], f[i & 1], c[j][i]);
+  }
+
+  // C += V^T P for one group, four M tiles at a time, so that their chains of
+  // three products overlap.
+  template <bool kOdd>
+  __device__ __forceinline__ void outputs(float (&c)[kM][4], const uint4 (&v)[kH][4], const uint32_t (&pb)[3][2]) {
+#pragma unroll
+    for (int j0 = 0; j0 < kM; j0 += 4) {
+      uint32_t av[4][4];
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {
+        // M rows gr and gr + 8 of tile j: dims 8 gr + j and 64 + 8 gr + j (DH 128), 8 gr + 2 j and 8 gr + 2 j + 1 (64)
+        const int j = j0 + jj;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int up = i & 1, pr = i >> 1;  // a0: rows gr, tokens 2t..; a1: rows gr + 8; a2, a3: tokens 2t + 8..
+          const uint32_t* ra = reinterpret_cast<const uint32_t*>(&v[kH == 2 ? up : 0][2 * pr]);
+          const uint32_t* rb = reinterpret_cast<const uint32_t*>(&v[kH == 2 ? up : 0][2 * pr + 1]);
+          const int word = kH == 2 ? j >> 1 : j;
+          const bool high = kH == 2 ? j & 1 : up;
+          av[jj][i] = __byte_perm(ra[word], rb[word], high ? 0x7632 : 0x5410);
+        }
+      }
+#pragma unroll
+      for (int s = 2; s >= 0; --s)
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+          if (kOdd && s > 0)
+            mma_bf16(c[j0 + jj], finite_halves(av[jj][0]), finite_halves(av[jj][1]), finite_halves(av[jj][2]),
+                     finite_halves(av[jj][3]), pb[s][0], pb[s][1]);
+          else
+            mma_bf16(c[j0 + jj], av[jj][0], av[jj][1], av[jj][2], av[jj][3], pb[s][0], pb[s][1]);
+        }
     }
   }
 
@@ -508,12 +608,12 @@ struct Bf16Rows {
 // of every head's query elements in registers; the GP heads' partial sums are
 // reduced over the 16 lanes by exchange steps that leave each lane one head.
 // Outputs: a lane holds DH / 32 dims of all heads and reads the row's weights
-// from shared memory.  GP: heads rounded up to a power of two.
+// from shared memory (where the stage's K rows were).  GP: heads rounded up to a power of two.
 template <int DH, int GP>
 struct F32Rows {
   static constexpr int kQ = DH / 64;      // float4 of a row per lane (logits)
   static constexpr int kD = DH / 32;      // dims per lane (outputs)
-  static constexpr int kRows = Ring<float, DH>::kRows;
+  static constexpr int kRows = kUnitRows<float, DH>;
   float4 q[GP][kQ];
   float o[GP][kD], m, l;
 
@@ -525,7 +625,8 @@ struct F32Rows {
     return h;
   }
 
-  __device__ __forceinline__ void start(const AttendArgs& a, int b, int h, int lane) {
+  __device__ __forceinline__ void start(const AttendArgs& a, int bh, int lane) {
+    const int b = bh / a.H, h = bh - b * a.H;
     const auto* qp = static_cast<const float*>(a.q) + b * a.qsb + (int64_t)(h * a.G) * a.qsh;
 #pragma unroll
     for (int g = 0; g < GP; ++g) {
@@ -540,9 +641,13 @@ struct F32Rows {
     l = 0.f;
   }
 
-  template <typename F>
-  __device__ __forceinline__ void step(const AttendArgs& a, const char* ks, const char* vs, float* p_smem, int valid,
-                                       float* xl, int lane, F refill) {
+  // The unit `in` holds next: `valid` rows (at least one); xl: their logits in
+  // global memory, or null.
+  __device__ __forceinline__ void step(const AttendArgs& a, Loader<float, DH>& in, int valid, float* xl, int lane) {
+    char* ks = in.take();
+    if (!ks) return;
+    const uint32_t have = in.groups();
+    float* p_smem = reinterpret_cast<float*>(ks);  // the rows' weights take the place of the K rows, once those are read
     const int half = lane >> 4, head = head_of(lane);
     float x[kRows / 2];
     float mx = -INFINITY;
@@ -574,7 +679,7 @@ struct F32Rows {
           v[0] += __shfl_xor_sync(0xffffffffu, v[0], s);
         }
       }
-      x[j] = row < valid ? v[0] * a.scale2 : -INFINITY;
+      x[j] = row < valid && (have >> (row / kGroup) & 1) ? v[0] * a.scale2 : -INFINITY;
       if (xl && row < valid && head < a.G && (lane & (16 / GP - 1)) == 0) xl[(int64_t)row * a.G + head] = x[j];
       mx = fmaxf(mx, x[j]);
     }
@@ -584,7 +689,7 @@ struct F32Rows {
     const float f = exp2f(m - mu);
     m = mx;
     l *= f;
-    __syncwarp();  // the last step's reads of p_smem
+    __syncwarp();  // every lane has read its K rows
 #pragma unroll
     for (int j = 0; j < kRows / 2; ++j) {
       const float p = exp2f(x[j] - mu);
@@ -609,6 +714,8 @@ struct F32Rows {
         for (int g = 0; g < GP; ++g) w[g] = pp[g];
       }
     };
+    const char* vs = in.take();
+    if (!vs) return;
     float w[GP];
     weights(kRows, w);
 #pragma unroll
@@ -618,6 +725,7 @@ struct F32Rows {
 #pragma unroll
     for (int row = 0; row < kRows; ++row) {
       if (row >= valid) break;  // rows behind the last hold anything
+      if (!(have >> (row / kGroup) & 1)) continue;
       const float* vr = reinterpret_cast<const float*>(vs + row * DH * 4) + lane * kD;
       float vx[kD];
       if constexpr (kD == 4) {
@@ -637,8 +745,10 @@ struct F32Rows {
 #pragma unroll
         for (int i = 0; i < kD; ++i) o[g][i] = fmaf(w[g], vx[i], o[g][i]);
     }
+    sm100::fence_async_smem();  // the weights were written by this thread, the next rows come by a bulk copy
     __syncwarp();
-    refill();
+    in.issue();
+    in.issue();
   }
 
   __device__ __forceinline__ void finish(Merge<DH>& mg, int warp, int lane) {
@@ -653,64 +763,62 @@ struct F32Rows {
   }
 };
 
-// One CTA per SM, 8 warps, a 24 KB ring each: up to 192 KB of rows in flight
-// per SM, several times what the memory latency needs at full bandwidth.
+// One CTA per SM, eight warps with a 24 KB ring each.
 template <typename E, int DH, typename Rows>
 __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(AttendArgs a) {
-  using R = Ring<E, DH>;
+  constexpr int kRows = kUnitRows<E, DH>;
   extern __shared__ __align__(128) char smem_raw[];
   auto& sm = *reinterpret_cast<AttendSmem<E, DH>*>(smem_raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (lane == 0) {
-    for (int i = 0; i < R::kStages; ++i) sm100::mbar_init(&sm.bar[warp][i], 1);
+    for (int i = 0; i < kSlots; ++i) sm100::mbar_init(&sm.bar[warp][i], 1);
     sm100::fence_mbar_init();
   }
-  __syncwarp();
+  if (threadIdx.x == 0) sm.dead = 0;
   sm100::grid_dep_wait();
   sm100::grid_dep_launch();
   Place at;
   bool empty;
   const int c = blockIdx.x;
-  const Cut cut = locate(a.c, a.BH, c, reinterpret_cast<int*>(sm.merge.o), at, empty);
+  const Cut cut = locate(a, c, reinterpret_cast<int*>(sm.merge.o), at, empty);
   if (c >= cut.g) return;
   const int u_end = cut.start(c + 1);
   int u = cut.start(c);
+  Rows rows;
+  rows.start(a, at.bh, lane);
+  static_assert(kLensTable == kThreads, "a thread per entry");
+  sm.lens[threadIdx.x] = at.bh + (int)threadIdx.x < a.BH ? a.c.len(at.bh + threadIdx.x) : 0;
+  __syncthreads();
+  const Lens lens{a.c, sm.lens, at.bh, a.unit_log};
   int mine = u + warp;  // this warp's next unit
-  Loader<E, DH> ld(a.c, sm, warp, lane, at, mine, u_end);
-  for (int i = 0; i < R::kStages; ++i) ld.issue();
-  for (bool first = true; u < u_end; first = false) {
-    seek(a.c, at, u);
-    const int ub = units_of(at.len);
+  Loader<E, DH> in(lens, sm, warp, lane, at, mine, u_end);
+  for (int i = 0; i < kSlots; ++i) in.issue();
+  int slot = 0;  // of a partial result: 1 but for the CTA's first segment
+#pragma unroll 1
+  while (u < u_end) {
+    const int ub = units_of(at.len, a.unit_log);
     const int ue = min(u_end, at.s + ub);
-    const int b = at.bh / a.H;
-    Rows rows;
-    rows.start(a, b, at.bh - b * a.H, lane);
+#pragma unroll 1
     for (; mine < ue; mine += kWarps) {
-#pragma unroll
-      for (int sub = 0; sub < R::kSub; ++sub) {
-        const int r = (mine - at.s) * kUnit + sub * R::kRows;
-        // (a unit's second stage may lie behind the last row: valid <= 0)
-        const int valid = min(at.len - r, R::kRows);
-        const int st = ld.take();
-        float* xl = a.w ? a.logits + ((int64_t)at.bh * a.c.max_len + r) * a.G : nullptr;
-        if (st >= 0) {
-          rows.step(a, sm.ring[warp][st][0], sm.ring[warp][st][1], &sm.p[warp][0][0], valid, xl, lane,
-                    [&] { ld.issue(); });
-        } else {
-          if (xl)
-            for (int i = lane; i < valid * a.G; i += 32) xl[i] = -INFINITY;
-          __syncwarp();
-          ld.issue();
-        }
-      }
+      const int r = (mine - at.s) * kRows;
+      float* xl = a.w ? a.logits + ((int64_t)at.bh * a.c.max_len + r) * a.G : nullptr;
+      rows.step(a, in, min(at.len - r, kRows), xl, lane);
     }
     rows.finish(sm.merge, warp, lane);
-    __syncthreads();
-    finish_segment<DH>(a, sm.merge, at.bh, u == at.s && ue == at.s + ub, first ? 0 : 1);
-    __syncthreads();
+    const int bh = at.bh;
+    const bool whole = u == at.s && ue == at.s + ub;
     u = ue;
+    if (u < u_end) {
+      // the next pair's queries are on their way while this one is reduced
+      lens.seek(at, u);
+      rows.start(a, at.bh, lane);
+    }
+    __syncthreads();
+    finish_segment<DH>(a, sm.merge, bh, whole, slot);
+    slot = 1;
+    __syncthreads();
   }
-  ld.drain();
+  in.drain();
 }
 
 // Join the partial results.  CTA j looks at the cut between ranges j and j + 1:
@@ -730,7 +838,7 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(AttendArgs a) {
   bool empty;
   // the lengths were final before the first kernel passed its own wait
   const int c = blockIdx.x + 1;
-  const Cut cut = locate(a.c, a.BH, c, sh_loc, at, empty);
+  const Cut cut = locate(a, c, sh_loc, at, empty);
   sm100::grid_dep_wait();
   sm100::grid_dep_launch();
   if (empty) {
@@ -742,7 +850,7 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(AttendArgs a) {
     }
   }
   if (c >= cut.g || cut.start(c) == at.s) return;
-  const int c0 = cut.range_of(at.s), np = cut.range_of(at.s + units_of(at.len) - 1) - c0 + 1;
+  const int c0 = cut.range_of(at.s), np = cut.range_of(at.s + units_of(at.len, a.unit_log) - 1) - c0 + 1;
   const int stride = kv_part_floats(a.G, DH);
   const int cols = a.G * DH / 4, share = c - c0 - 1;
   const int q0 = cols * share / (np - 1), nq = cols * (share + 1) / (np - 1) - q0;
@@ -892,7 +1000,9 @@ cudaError_t launch_kv_attend(const Plan& p, const KvView& c, const void* q, int6
   a.part = (float*)(base + L.part);
   a.lse2 = (float*)(base + L.lse2);
   a.logits = (float*)(base + L.logits);
-  const int64_t most = a.BH * ceil_div64(c.max_len, kUnit);
+  const int unit = kSlotBytes / (cfg.d_h * p.esize);
+  a.unit_log = unit == 64 ? 6 : unit == 32 ? 5 : 4;
+  const int64_t most = a.BH * ceil_div64(c.max_len, unit);
   const int grid = (int)std::min<int64_t>(kKvMaxGrid, ceil_div64(most, kMinUnits));
   if (!p.bf16) return cfg.d_h == 128 ? launch_f32<128>(p, a, grid, st) : launch_f32<64>(p, a, grid, st);
   return cfg.d_h == 128 ? launch_t<__nv_bfloat16, 128, Bf16Rows<128>>(p, a, grid, st)
