@@ -79,8 +79,10 @@ __device__ __forceinline__ int units_of(int len, int unit_log) { return (len + (
 // over the lengths.  Every thread returns the same values; sh: kLocateWords
 // of shared memory, free again on return.  Lengths out of range are reported
 // here; `empty` tells whether any pair holds no row.
+// Where a thread has one pair at most, it leaves its length in table (if not
+// null).
 constexpr int kLocateWords = kWarps + 4;
-__device__ __forceinline__ Cut locate(const AttendArgs& a, int c, int* sh, Place& at, bool& empty) {
+__device__ __forceinline__ Cut locate(const AttendArgs& a, int c, int* sh, int* table, Place& at, bool& empty) {
   const KvView& k = a.c;
   const int BH = a.BH;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -94,13 +96,14 @@ __device__ __forceinline__ Cut locate(const AttendArgs& a, int c, int* sh, Place
     none |= last == 0;
     sum += units_of(last, a.unit_log);
   }
+  if (table) table[tid] = last;
   int inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += v;
   }
-  if (lane == 31 && warp < kWarps) sh[warp] = inc;
+  if (lane == 31) sh[warp] = inc;
   empty = __syncthreads_or(none) != 0;
   int before = 0, W = 0;
 #pragma unroll
@@ -156,12 +159,15 @@ struct Lens {
   }
 };
 
-// One warp's running softmax over its rows, as partial results: m, l and o
-// per head, reduced over the block's warps in shared memory.
-template <int DH>
+// The warps' partial results of up to kBufs segments, heads padded to GP: a
+// warp leaves a segment's result and goes on to the next segment's rows, and
+// the block meets once for all of them.
+template <int DH, int GP>
 struct Merge {
-  float m[kWarps][kMaxG], l[kWarps][kMaxG];
-  float o[kWarps][kMaxG][DH];
+  static constexpr int kBufs = GP >= 4 ? 8 / GP : 4;
+  float m[kBufs][kWarps][GP], l[kBufs][kWarps][GP];
+  float o[kBufs][kWarps][GP][DH];
+  int bh[kBufs], slot[kBufs];  // whose part it is; partial slot, or -1 where the segment is the whole pair
 };
 
 // Four dims of one head's result; the thread of a head's first dims also
@@ -179,34 +185,46 @@ __device__ __forceinline__ void write_out(const AttendArgs& a, int bh, int b, in
   }
 }
 
-// Reduce the warps' parts of one segment and write them where they belong:
-// out and lse where the segment is the whole pair, else the partial slot.
-template <int DH>
-__device__ __forceinline__ void finish_segment(const AttendArgs& a, const Merge<DH>& sm, int bh, bool whole, int slot) {
-  const int b = bh / a.H, h = bh - b * a.H;
-  float* part = a.part + (blockIdx.x * 2 + slot) * (int64_t)kv_part_floats(a.G, DH);
-  for (int i = threadIdx.x * 4; i < a.G * DH; i += kThreads * 4) {
-    const int g = i / DH, e = i % DH;
-    float m = -INFINITY;
+// Reduce the warps' parts of a segment: thread i's four dims (i < GP DH / 4).
+template <int DH, int GP>
+__device__ __forceinline__ void reduce_warps(const Merge<DH, GP>& sm, int buf, int g, int e, float& m, float& l,
+                                             float4& o) {
+  m = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.m[w][g]);
-    const float mu = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.m[buf][w][g]);
+  const float mu = m == -INFINITY ? 0.f : m;
+  l = 0.f;
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = exp2f(sm.m[w][g] - mu);
-      const float4 v = *reinterpret_cast<const float4*>(&sm.o[w][g][e]);
-      l = fmaf(sm.l[w][g], f, l);
-      o.x = fmaf(v.x, f, o.x);
-      o.y = fmaf(v.y, f, o.y);
-      o.z = fmaf(v.z, f, o.z);
-      o.w = fmaf(v.w, f, o.w);
-    }
-    if (whole) {
-      write_out<DH>(a, bh, b, h, g, e, m, l, o);
+  for (int w = 0; w < kWarps; ++w) {
+    const float f = exp2f(sm.m[buf][w][g] - mu);
+    const float4 v = *reinterpret_cast<const float4*>(&sm.o[buf][w][g][e]);
+    l = fmaf(sm.l[buf][w][g], f, l);
+    o.x = fmaf(v.x, f, o.x);
+    o.y = fmaf(v.y, f, o.y);
+    o.z = fmaf(v.z, f, o.z);
+    o.w = fmaf(v.w, f, o.w);
+  }
+}
+
+// Reduce `n` segments and write them where they belong: out and lse where a
+// segment is the whole pair, else its partial slot.
+template <int DH, int GP>
+__device__ __forceinline__ void finish_segments(const AttendArgs& a, const Merge<DH, GP>& sm, int n) {
+  const int per = a.G * DH / 4;  // threads per segment
+#pragma unroll 1
+  for (int i = threadIdx.x; i < n * per; i += kThreads) {
+    const int buf = i / per, q = i - buf * per, g = q / (DH / 4), e = q % (DH / 4) * 4;
+    float m, l;
+    float4 o;
+    reduce_warps(sm, buf, g, e, m, l, o);
+    const int bh = sm.bh[buf], slot = sm.slot[buf];
+    if (slot < 0) {
+      const int b = bh / a.H;
+      write_out<DH>(a, bh, b, bh - b * a.H, g, e, m, l, o);
     } else {
-      *reinterpret_cast<float4*>(part + i) = o;
+      float* part = a.part + (blockIdx.x * 2 + slot) * (int64_t)kv_part_floats(a.G, DH);
+      *reinterpret_cast<float4*>(part + q * 4) = o;
       if (e == 0) {
         part[a.G * DH + g] = m;
         part[a.G * DH + kMaxG + g] = l;
@@ -224,13 +242,17 @@ __device__ __forceinline__ void finish_segment(const AttendArgs& a, const Merge<
 // between the segments' ends.  Plain copies in this pattern reach 7.3 TB/s with
 // 8 KB copies and 96 to 128 KB in flight per SM, 6.6 with 4 KB copies and 192
 // KB, 5.3 with 2 KB copies.
-template <typename E, int DH>
-struct AttendSmem {
+struct RingSmem {
   alignas(128) char ring[kWarps][kSlots][kSlotBytes];
-  Merge<DH> merge;
   int lens[kLensTable];
   uint64_t bar[kWarps][kSlots];
   int dead;  // a wait ran out: nothing more is issued or waited for
+};
+
+template <int DH, int GP>
+struct AttendSmem {
+  RingSmem ring;
+  Merge<DH, GP> merge;
 };
 
 template <typename E, int DH>
@@ -240,7 +262,7 @@ struct Loader {
   static constexpr int kRowBytes = DH * (int)sizeof(E);
   static constexpr int kBatch = 32 / kGroups;     // units looked up at a time
   const Lens& lens;
-  AttendSmem<E, DH>& sm;
+  RingSmem& sm;
   const int warp, lane, u_end;
   // The warp's units kBatch at a time: lane i looks up group i % kGroups of the
   // (i / kGroups)-th of them (its pair, then its page), all at once; off: the
@@ -255,7 +277,7 @@ struct Loader {
   uint32_t good = 0;       // bit k of units issued last in the high bits: group k's rows are there
   bool dead = false;
 
-  __device__ __forceinline__ Loader(const Lens& l_, AttendSmem<E, DH>& s_, int w, int l, Place p, int u, int e)
+  __device__ __forceinline__ Loader(const Lens& l_, RingSmem& s_, int w, int l, Place p, int u, int e)
       : lens(l_), sm(s_), warp(w), lane(l), u_end(e), u0(u), at(p) {
     look();
   }
@@ -388,16 +410,22 @@ __device__ __forceinline__ uint32_t finite_halves(uint32_t v) {
 //    2t+8, 2t+9 hold its operands once the two rows of a pair are interleaved
 //    (byte permutes); P comes out of X's accumulators by an 8x8 transpose.
 //  - P in three bfloat16 terms (24 bits of it): with one, each weight would
-//    carry 2^-8 into a float32 result.  The extra products cost little: the
-//    tensor pipe is far from full.  An infinite V element must meet the first
-//    term only (the others may be zero or negative), so the others take V with
-//    such elements zeroed where a step has any.
+//    carry 2^-8 into a float32 result.  With GP = 4 heads the second term goes
+//    into the columns 4 .. 7 of the first one's product, and with GP = 2 all
+//    three into one product: queries repeat over the columns, so that every
+//    lane has the weights at hand, and the columns of a head are added up at
+//    the segment's end.  An infinite V element must meet the first term only
+//    (the others may be zero or negative): where a group has any, the terms
+//    take V with such elements zeroed and one more product adds them, times the
+//    first term.
 //  - A step's products go into zeroed accumulators that are then added to the
 //    running ones in float32: the tensor core's own additions may truncate,
 //    which over thousands of steps would bias the sums.
-template <int DH>
+template <int DH, int GP_>
 struct Bf16Rows {
   using E = __nv_bfloat16;
+  static constexpr int GP = GP_;           // 2, 4 or 8: heads per copy of them in the columns
+  static constexpr int kTerms = GP == 8 ? 3 : GP == 4 ? 2 : 1;  // products per group
   static constexpr int kG = kUnitRows<E, DH> / kGroup;
   static constexpr int kW = DH / 32;       // 16-byte words of a K row per lane
   static constexpr int kM = DH / 16;       // M tiles of O
@@ -408,11 +436,12 @@ struct Bf16Rows {
   __device__ __forceinline__ void start(const AttendArgs& a, int bh, int lane) {
     const int b = bh / a.H, h = bh - b * a.H;
     const int gr = lane >> 2, t = lane & 3;
-    const auto* qp = static_cast<const E*>(a.q) + b * a.qsb + (int64_t)(h * a.G + gr) * a.qsh;
+    const int head = gr & (GP - 1);
+    const auto* qp = static_cast<const E*>(a.q) + b * a.qsb + (int64_t)(h * a.G + head) * a.qsh;
 #pragma unroll
     for (int i = 0; i < kW; ++i) {
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (gr < a.G) v = __ldcg(reinterpret_cast<const uint4*>(qp) + i * 4 + t);
+      if (head < a.G) v = __ldcg(reinterpret_cast<const uint4*>(qp) + i * 4 + t);
       q[i][0] = v.x;
       q[i][1] = v.y;
       q[i][2] = v.z;
@@ -456,13 +485,21 @@ struct Bf16Rows {
         for (int i = 0; i < 4; ++i)
           if (n * kGroup + gr + (i >> 1) * 8 >= valid || !(have >> n & 1)) x[n][i] = -INFINITY;
     }
-    if (xl) {
+    if (xl && 2 * t < a.G && 2 * t < GP) {
+      const bool two = (a.G & 1) == 0;  // both heads of the lane in one store
 #pragma unroll
       for (int n = 0; n < kG; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = n * kGroup + gr + (i >> 1) * 8, g = 2 * t + (i & 1);
-          if (row < valid && g < a.G) xl[(int64_t)row * a.G + g] = x[n][i];
+        for (int hf = 0; hf < 2; ++hf) {
+          const int row = n * kGroup + gr + hf * 8;
+          if (row >= valid) continue;
+          float* xp = xl + row * a.G + 2 * t;
+          if (two) {
+            *reinterpret_cast<float2*>(xp) = make_float2(x[n][2 * hf], x[n][2 * hf + 1]);
+          } else {
+            xp[0] = x[n][2 * hf];
+            if (2 * t + 1 < a.G) xp[1] = x[n][2 * hf + 1];
+          }
         }
     }
     float f[2];
@@ -485,18 +522,29 @@ struct Bf16Rows {
         l[c] += x[n][c] + x[n][c + 2];
       }
     }
-    uint32_t pb[kG][3][2];
+    uint32_t p1[kG][2], pb[kG][kTerms][2];  // the first term, not yet transposed; the products' P
 #pragma unroll
     for (int n = 0; n < kG; ++n)
 #pragma unroll
-      for (int s = 0; s < 3; ++s)
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t w[3];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const uint32_t w = pack_bf16(x[n][2 * hf], x[n][2 * hf + 1]);
-          x[n][2 * hf] -= lo_f(w);
-          x[n][2 * hf + 1] -= hi_f(w);
-          pb[n][s][hf] = transpose8(w);
+        for (int s = 0; s < 3; ++s) {
+          w[s] = pack_bf16(x[n][2 * hf], x[n][2 * hf + 1]);
+          x[n][2 * hf] -= lo_f(w[s]);
+          x[n][2 * hf + 1] -= hi_f(w[s]);
         }
+        p1[n][hf] = w[0];
+        if constexpr (GP == 8) {
+#pragma unroll
+          for (int s = 0; s < 3; ++s) pb[n][s][hf] = transpose8(w[s]);
+        } else if constexpr (GP == 4) {
+          pb[n][0][hf] = transpose8(t < 2 ? w[0] : w[1]);
+          pb[n][1][hf] = transpose8(t < 2 ? w[2] : 0u);
+        } else {
+          pb[n][0][hf] = transpose8(t == 0 ? w[0] : t == 1 ? w[1] : t == 2 ? w[2] : 0u);
+        }
+      }
     const char* vs = in.take();
     if (!vs) return;
     float c[kM][4];
@@ -531,9 +579,9 @@ struct Bf16Rows {
         }
       // the halves are zero or NaN
       if (!__any_sync(0xffffffffu, ((nz[0] | nz[1] | nz[2] | nz[3]) & 0x7fff7fffu) != 0u))
-        outputs<false>(c, v, pb[n]);
+        outputs<false>(c, v, p1[n], pb[n]);
       else
-        outputs<true>(c, v, pb[n]);
+        outputs<true>(c, v, p1[n], pb[n]);
     }
 #pragma unroll
     for (int j = 0; j < kM; ++j)
@@ -542,9 +590,15 @@ struct Bf16Rows {
   }
 
   // C += V^T P for one group, four M tiles at a time, so that their chains of
-  // three products overlap.
+  // products overlap.
   template <bool kOdd>
-  __device__ __forceinline__ void outputs(float (&c)[kM][4], const uint4 (&v)[kH][4], const uint32_t (&pb)[3][2]) {
+  __device__ __forceinline__ void outputs(float (&c)[kM][4], const uint4 (&v)[kH][4], const uint32_t (&p1)[2],
+                                          const uint32_t (&pb)[kTerms][2]) {
+    uint32_t ph[2] = {0u, 0u};
+    if (kOdd) {
+      ph[0] = transpose8(p1[0]);
+      ph[1] = transpose8(p1[1]);
+    }
 #pragma unroll
     for (int j0 = 0; j0 < kM; j0 += 4) {
       uint32_t av[4][4];
@@ -562,31 +616,53 @@ struct Bf16Rows {
           av[jj][i] = __byte_perm(ra[word], rb[word], high ? 0x7632 : 0x5410);
         }
       }
-#pragma unroll
-      for (int s = 2; s >= 0; --s)
+      if (kOdd) {
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
-          if (kOdd && s > 0)
-            mma_bf16(c[j0 + jj], finite_halves(av[jj][0]), finite_halves(av[jj][1]), finite_halves(av[jj][2]),
-                     finite_halves(av[jj][3]), pb[s][0], pb[s][1]);
-          else
-            mma_bf16(c[j0 + jj], av[jj][0], av[jj][1], av[jj][2], av[jj][3], pb[s][0], pb[s][1]);
+          uint32_t od[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t fin = finite_halves(av[jj][i]);
+            od[i] = av[jj][i] ^ fin;  // the infinite and NaN halves
+            av[jj][i] = fin;
+          }
+          mma_bf16(c[j0 + jj], od[0], od[1], od[2], od[3], ph[0], ph[1]);
         }
+      }
+#pragma unroll
+      for (int s = kTerms - 1; s >= 0; --s)
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj)
+          mma_bf16(c[j0 + jj], av[jj][0], av[jj][1], av[jj][2], av[jj][3], pb[s][0], pb[s][1]);
     }
   }
 
-  __device__ __forceinline__ void finish(Merge<DH>& mg, int warp, int lane) {
+  __device__ __forceinline__ void finish(Merge<DH, GP>& mg, int buf, int warp, int lane) {
     const int gr = lane >> 2, t = lane & 3;
+    // add up the columns of a head
+    if constexpr (GP < 8) {
+#pragma unroll
+      for (int j = 0; j < kM; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[j][i] += __shfl_xor_sync(0xffffffffu, o[j][i], 2);
+          if (GP == 2) o[j][i] += __shfl_xor_sync(0xffffffffu, o[j][i], 1);
+        }
+    }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       l[c] += __shfl_xor_sync(0xffffffffu, l[c], 4);
       l[c] += __shfl_xor_sync(0xffffffffu, l[c], 8);
       l[c] += __shfl_xor_sync(0xffffffffu, l[c], 16);
+    }
+    if (2 * t >= GP) return;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
       if (gr == 0) {
-        mg.m[warp][2 * t + c] = m[c];
-        mg.l[warp][2 * t + c] = l[c];
+        mg.m[buf][warp][2 * t + c] = m[c];
+        mg.l[buf][warp][2 * t + c] = l[c];
       }
-      float* op = mg.o[warp][2 * t + c] + gr * 8;
+      float* op = mg.o[buf][warp][2 * t + c] + gr * 8;
       if constexpr (DH == 128) {
 #pragma unroll
         for (int w = 0; w < 2; ++w)
@@ -609,8 +685,10 @@ struct Bf16Rows {
 // reduced over the 16 lanes by exchange steps that leave each lane one head.
 // Outputs: a lane holds DH / 32 dims of all heads and reads the row's weights
 // from shared memory (where the stage's K rows were).  GP: heads rounded up to a power of two.
-template <int DH, int GP>
+template <int DH, int GP_>
 struct F32Rows {
+  using E = float;
+  static constexpr int GP = GP_;
   static constexpr int kQ = DH / 64;      // float4 of a row per lane (logits)
   static constexpr int kD = DH / 32;      // dims per lane (outputs)
   static constexpr int kRows = kUnitRows<float, DH>;
@@ -751,49 +829,58 @@ struct F32Rows {
     in.issue();
   }
 
-  __device__ __forceinline__ void finish(Merge<DH>& mg, int warp, int lane) {
+  __device__ __forceinline__ void finish(Merge<DH, GP>& mg, int buf, int warp, int lane) {
     l += __shfl_xor_sync(0xffffffffu, l, 16);
     const int head = head_of(lane);
-    mg.m[warp][head] = m;
-    mg.l[warp][head] = l;
+    mg.m[buf][warp][head] = m;
+    mg.l[buf][warp][head] = l;
 #pragma unroll
     for (int g = 0; g < GP; ++g)
 #pragma unroll
-      for (int i = 0; i < kD; ++i) mg.o[warp][g][lane * kD + i] = o[g][i];
+      for (int i = 0; i < kD; ++i) mg.o[buf][warp][g][lane * kD + i] = o[g][i];
   }
 };
 
-// One CTA per SM, eight warps with a 24 KB ring each.
-template <typename E, int DH, typename Rows>
-__global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(AttendArgs a) {
-  constexpr int kRows = kUnitRows<E, DH>;
-  extern __shared__ __align__(128) char smem_raw[];
-  auto& sm = *reinterpret_cast<AttendSmem<E, DH>*>(smem_raw);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ void init_ring(RingSmem& ring, int warp, int lane) {
   if (lane == 0) {
-    for (int i = 0; i < kSlots; ++i) sm100::mbar_init(&sm.bar[warp][i], 1);
+    for (int i = 0; i < kSlots; ++i) sm100::mbar_init(&ring.bar[warp][i], 1);
     sm100::fence_mbar_init();
   }
-  if (threadIdx.x == 0) sm.dead = 0;
+  if (threadIdx.x == 0) ring.dead = 0;
+}
+
+// One CTA per SM, eight warps with a 24 KB ring each.
+template <int DH, typename Rows>
+__global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_constant__ AttendArgs a) {
+  using E = typename Rows::E;
+  constexpr int kRows = kUnitRows<E, DH>;
+  using M = Merge<DH, Rows::GP>;
+  extern __shared__ __align__(128) char smem_raw[];
+  auto& sm = *reinterpret_cast<AttendSmem<DH, Rows::GP>*>(smem_raw);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  init_ring(sm.ring, warp, lane);
   sm100::grid_dep_wait();
   sm100::grid_dep_launch();
   Place at;
   bool empty;
   const int c = blockIdx.x;
-  const Cut cut = locate(a, c, reinterpret_cast<int*>(sm.merge.o), at, empty);
+  const Cut cut = locate(a, c, reinterpret_cast<int*>(sm.merge.o), sm.ring.lens, at, empty);
   if (c >= cut.g) return;
-  const int u_end = cut.start(c + 1);
-  int u = cut.start(c);
+  const int u_first = cut.start(c), u_end = cut.start(c + 1);
   Rows rows;
   rows.start(a, at.bh, lane);
   static_assert(kLensTable == kThreads, "a thread per entry");
-  sm.lens[threadIdx.x] = at.bh + (int)threadIdx.x < a.BH ? a.c.len(at.bh + threadIdx.x) : 0;
-  __syncthreads();
-  const Lens lens{a.c, sm.lens, at.bh, a.unit_log};
-  int mine = u + warp;  // this warp's next unit
-  Loader<E, DH> in(lens, sm, warp, lane, at, mine, u_end);
+  int bh0 = 0;  // locate() has left the lengths where they fit the table
+  if (a.BH > kLensTable) {
+    bh0 = at.bh;
+    sm.ring.lens[threadIdx.x] = bh0 + (int)threadIdx.x < a.BH ? a.c.len(bh0 + threadIdx.x) : 0;
+    __syncthreads();
+  }
+  const Lens lens{a.c, sm.ring.lens, bh0, a.unit_log};
+  int u = u_first, mine = u + warp;  // this warp's next unit
+  Loader<E, DH> in(lens, sm.ring, warp, lane, at, mine, u_end);
   for (int i = 0; i < kSlots; ++i) in.issue();
-  int slot = 0;  // of a partial result: 1 but for the CTA's first segment
+  int held = 0;  // segments in the merge buffers
 #pragma unroll 1
   while (u < u_end) {
     const int ub = units_of(at.len, a.unit_log);
@@ -804,19 +891,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(AttendArgs a) {
       float* xl = a.w ? a.logits + ((int64_t)at.bh * a.c.max_len + r) * a.G : nullptr;
       rows.step(a, in, min(at.len - r, kRows), xl, lane);
     }
-    rows.finish(sm.merge, warp, lane);
-    const int bh = at.bh;
-    const bool whole = u == at.s && ue == at.s + ub;
-    u = ue;
-    if (u < u_end) {
-      // the next pair's queries are on their way while this one is reduced
-      lens.seek(at, u);
-      rows.start(a, at.bh, lane);
+    rows.finish(sm.merge, held, warp, lane);
+    if (threadIdx.x == 0) {
+      sm.merge.bh[held] = at.bh;
+      sm.merge.slot[held] = u == at.s && ue == at.s + ub ? -1 : u == u_first ? 0 : 1;
     }
-    __syncthreads();
-    finish_segment<DH>(a, sm.merge, bh, whole, slot);
-    slot = 1;
-    __syncthreads();
+    ++held;
+    u = ue;
+    // the next pair's queries are on their way while this one is reduced (after the last, the same pair's again)
+    lens.seek(at, min(u, u_end - 1));
+    rows.start(a, at.bh, lane);
+    if (held == M::kBufs || u >= u_end) {
+      __syncthreads();
+      finish_segments(a, sm.merge, held);
+      __syncthreads();
+      held = 0;
+    }
   }
   in.drain();
 }
@@ -829,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(AttendArgs a) {
 // not depend on timing).  One round trip to L2 after the attention's end; the
 // search for the cut runs before it.
 template <int DH>
-__global__ void __launch_bounds__(kThreads) kv_join_kernel(AttendArgs a) {
+__global__ void __launch_bounds__(kThreads) kv_join_kernel(const __grid_constant__ AttendArgs a) {
   __shared__ int sh_loc[kLocateWords];
   __shared__ float2 sh_ml[kThreads];
   __shared__ float4 sh_o[kThreads];
@@ -838,7 +928,7 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(AttendArgs a) {
   bool empty;
   // the lengths were final before the first kernel passed its own wait
   const int c = blockIdx.x + 1;
-  const Cut cut = locate(a, c, sh_loc, at, empty);
+  const Cut cut = locate(a, c, sh_loc, nullptr, at, empty);
   sm100::grid_dep_wait();
   sm100::grid_dep_launch();
   if (empty) {
@@ -905,7 +995,7 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(AttendArgs a) {
 // it reads and writes (4 G + 8 bytes a row).
 constexpr int kWeightRows = 4 * kThreads;
 
-__global__ void __launch_bounds__(kThreads) kv_weights_kernel(AttendArgs a, int chunks) {
+__global__ void __launch_bounds__(kThreads) kv_weights_kernel(const __grid_constant__ AttendArgs a, int chunks) {
   const int bh = blockIdx.x / chunks, r0 = (blockIdx.x - bh * chunks) * kWeightRows + threadIdx.x;
   const int len = a.c.len(bh);  // final before the first kernel of the call passed its wait
   sm100::grid_dep_wait();
@@ -942,10 +1032,10 @@ cudaError_t allow_smem(const void* kern, size_t smem, std::atomic<uint64_t>& rea
   return e;
 }
 
-template <typename E, int DH, typename Rows>
+template <int DH, typename Rows>
 cudaError_t launch_t(const Plan& p, const AttendArgs& a, int grid, cudaStream_t st) {
-  auto kern = kv_attend_kernel<E, DH, Rows>;
-  constexpr size_t smem = sizeof(AttendSmem<E, DH>);
+  auto kern = kv_attend_kernel<DH, Rows>;
+  constexpr size_t smem = sizeof(AttendSmem<DH, Rows::GP>);
   static_assert(smem <= 227 * 1024, "shared memory of one CTA");
   static std::atomic<uint64_t> ready{0};  // a bit per device: the attribute is the device's
   cudaError_t e = allow_smem((const void*)kern, smem, ready);
@@ -966,11 +1056,16 @@ cudaError_t launch_t(const Plan& p, const AttendArgs& a, int grid, cudaStream_t 
 }
 
 template <int DH>
-cudaError_t launch_f32(const Plan& p, const AttendArgs& a, int grid, cudaStream_t st) {
-  if (a.G == 1) return launch_t<float, DH, F32Rows<DH, 1>>(p, a, grid, st);
-  if (a.G == 2) return launch_t<float, DH, F32Rows<DH, 2>>(p, a, grid, st);
-  if (a.G <= 4) return launch_t<float, DH, F32Rows<DH, 4>>(p, a, grid, st);
-  return launch_t<float, DH, F32Rows<DH, 8>>(p, a, grid, st);
+cudaError_t launch_d(const Plan& p, const AttendArgs& a, int grid, cudaStream_t st) {
+  if (p.bf16) {
+    if (a.G <= 2) return launch_t<DH, Bf16Rows<DH, 2>>(p, a, grid, st);
+    if (a.G <= 4) return launch_t<DH, Bf16Rows<DH, 4>>(p, a, grid, st);
+    return launch_t<DH, Bf16Rows<DH, 8>>(p, a, grid, st);
+  }
+  if (a.G == 1) return launch_t<DH, F32Rows<DH, 1>>(p, a, grid, st);
+  if (a.G == 2) return launch_t<DH, F32Rows<DH, 2>>(p, a, grid, st);
+  if (a.G <= 4) return launch_t<DH, F32Rows<DH, 4>>(p, a, grid, st);
+  return launch_t<DH, F32Rows<DH, 8>>(p, a, grid, st);
 }
 
 }  // namespace
@@ -1004,9 +1099,7 @@ cudaError_t launch_kv_attend(const Plan& p, const KvView& c, const void* q, int6
   a.unit_log = unit == 64 ? 6 : unit == 32 ? 5 : 4;
   const int64_t most = a.BH * ceil_div64(c.max_len, unit);
   const int grid = (int)std::min<int64_t>(kKvMaxGrid, ceil_div64(most, kMinUnits));
-  if (!p.bf16) return cfg.d_h == 128 ? launch_f32<128>(p, a, grid, st) : launch_f32<64>(p, a, grid, st);
-  return cfg.d_h == 128 ? launch_t<__nv_bfloat16, 128, Bf16Rows<128>>(p, a, grid, st)
-                        : launch_t<__nv_bfloat16, 64, Bf16Rows<64>>(p, a, grid, st);
+  return cfg.d_h == 128 ? launch_d<128>(p, a, grid, st) : launch_d<64>(p, a, grid, st);
 }
 
 }  // namespace dkv
