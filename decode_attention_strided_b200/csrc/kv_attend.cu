@@ -680,27 +680,40 @@ struct Bf16Rows {
 };
 
 // float32 rows on the CUDA cores (float32 results leave no room for tf32's
-// 2^-11).  Logits: half a warp per row, a lane holds DH / 16 of the row's and
-// of every head's query elements in registers; the GP heads' partial sums are
-// reduced over the 16 lanes by exchange steps that leave each lane one head.
-// Outputs: a lane holds DH / 32 dims of all heads and reads the row's weights
-// from shared memory (where the stage's K rows were).  GP: heads rounded up to a power of two.
+// 2^-11).  Logits: kL lanes per row, a lane holds DH / kL elements of every
+// head's query in registers (64 at most: kL is 4 to 16 by the heads); the GP
+// heads' partial sums are reduced over the kL lanes by exchange steps that
+// leave each lane one head.  Outputs: a lane holds four dims of all heads and
+// reads the rows' weights from shared memory (where the unit's K rows were).
+// GP: heads rounded up to a power of two.
 template <int DH, int GP_>
 struct F32Rows {
   using E = float;
   static constexpr int GP = GP_;
-  static constexpr int kQ = DH / 64;      // float4 of a row per lane (logits)
-  static constexpr int kD = DH / 32;      // dims per lane (outputs)
   static constexpr int kRows = kUnitRows<float, DH>;
-  float4 q[GP][kQ];
-  float o[GP][kD], m, l;
+  static constexpr int kL = DH * GP / 64 < 4 ? 4 : DH * GP / 64;  // 4, 8 or 16
+  static constexpr int kC = DH / (4 * kL);                        // 16-byte words of a row per lane
+  static constexpr int kPer = 32 / kL;                            // rows per pass
+  static constexpr int kPasses = kRows / kPer;
+  static constexpr int kV = DH / 4;                               // lanes per V row: 32 or 16
+  static_assert(GP <= kL && kL <= 16 && kRows % kPer == 0, "");
+  float4 q[GP][kC], o[GP];
+  float m, l;
 
   __device__ __forceinline__ static int head_of(int lane) {
-    int h = 0;
-    if constexpr (GP == 8) h = ((lane & 8) ? 4 : 0) | ((lane & 4) ? 2 : 0) | ((lane & 2) ? 1 : 0);
-    if constexpr (GP == 4) h = ((lane & 8) ? 2 : 0) | ((lane & 4) ? 1 : 0);
-    if constexpr (GP == 2) h = (lane & 8) ? 1 : 0;
+    int n = GP, h = 0;
+#pragma unroll
+    for (int s = kL / 2; s > 0; s >>= 1)
+      if (n > 1) {
+        n >>= 1;
+        h += (lane & s) ? n : 0;
+      }
     return h;
+  }
+  // the i-th word of a row that a lane holds; with four lanes per row, the rows of a pair take their words in opposite
+  // order of halves, so that eight lanes' reads meet all banks
+  __device__ __forceinline__ static int word_of(int i, int lane) {
+    return (i * kL + lane % kL) ^ (kL == 4 && (lane / kL & 1) ? kL : 0);
   }
 
   __device__ __forceinline__ void start(const AttendArgs& a, int bh, int lane) {
@@ -709,11 +722,10 @@ struct F32Rows {
 #pragma unroll
     for (int g = 0; g < GP; ++g) {
 #pragma unroll
-      for (int i = 0; i < kQ; ++i)
-        q[g][i] = g < a.G ? __ldcg(reinterpret_cast<const float4*>(qp + g * a.qsh) + i * 16 + (lane & 15))
+      for (int i = 0; i < kC; ++i)
+        q[g][i] = g < a.G ? __ldcg(reinterpret_cast<const float4*>(qp + g * a.qsh) + word_of(i, lane))
                           : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < kD; ++i) o[g][i] = 0.f;
+      o[g] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     m = -INFINITY;
     l = 0.f;
@@ -726,25 +738,25 @@ struct F32Rows {
     if (!ks) return;
     const uint32_t have = in.groups();
     float* p_smem = reinterpret_cast<float*>(ks);  // the rows' weights take the place of the K rows, once those are read
-    const int half = lane >> 4, head = head_of(lane);
-    float x[kRows / 2];
-    float mx = -INFINITY;
+    const int head = head_of(lane);
+    float x[kPasses];
+    float mx = m;
 #pragma unroll
-    for (int j = 0; j < kRows / 2; ++j) {
-      const int row = 2 * j + half;
+    for (int j = 0; j < kPasses; ++j) {
+      const int row = j * kPer + lane / kL;
       float v[GP];
 #pragma unroll
       for (int g = 0; g < GP; ++g) v[g] = 0.f;
 #pragma unroll
-      for (int i = 0; i < kQ; ++i) {
-        const float4 kx = *reinterpret_cast<const float4*>(ks + row * DH * 4 + (i * 16 + (lane & 15)) * 16);
+      for (int i = 0; i < kC; ++i) {
+        const float4 kx = *reinterpret_cast<const float4*>(ks + row * DH * 4 + word_of(i, lane) * 16);
 #pragma unroll
         for (int g = 0; g < GP; ++g)
           v[g] = fmaf(q[g][i].x, kx.x, fmaf(q[g][i].y, kx.y, fmaf(q[g][i].z, kx.z, fmaf(q[g][i].w, kx.w, v[g]))));
       }
       int n = GP;
 #pragma unroll
-      for (int s = 8; s > 0; s >>= 1) {
+      for (int s = kL / 2; s > 0; s >>= 1) {
         if (n > 1) {
           n >>= 1;
 #pragma unroll
@@ -757,71 +769,56 @@ struct F32Rows {
           v[0] += __shfl_xor_sync(0xffffffffu, v[0], s);
         }
       }
-      x[j] = row < valid && (have >> (row / kGroup) & 1) ? v[0] * a.scale2 : -INFINITY;
-      if (xl && row < valid && head < a.G && (lane & (16 / GP - 1)) == 0) xl[(int64_t)row * a.G + head] = x[j];
-      mx = fmaxf(mx, x[j]);
+      x[j] = v[0] * a.scale2;
     }
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-    mx = fmaxf(mx, m);
+    const bool full = valid == kRows && have == (1u << (kRows / kGroup)) - 1;
+    if (!full) {
+      // rows that do not count: whatever the slot holds
+#pragma unroll
+      for (int j = 0; j < kPasses; ++j) {
+        const int row = j * kPer + lane / kL;
+        if (row >= valid || !(have >> (row / kGroup) & 1)) x[j] = -INFINITY;
+      }
+    }
+    if (xl && head < a.G && (lane & (kL / GP - 1)) == 0) {
+#pragma unroll
+      for (int j = 0; j < kPasses; ++j) {
+        const int row = j * kPer + lane / kL;
+        if (row < valid) xl[row * a.G + head] = x[j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kPasses; ++j) mx = fmaxf(mx, x[j]);
+#pragma unroll
+    for (int s = kL; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
     const float mu = mx == -INFINITY ? 0.f : mx;
     const float f = exp2f(m - mu);
     m = mx;
     l *= f;
     __syncwarp();  // every lane has read its K rows
 #pragma unroll
-    for (int j = 0; j < kRows / 2; ++j) {
+    for (int j = 0; j < kPasses; ++j) {
       const float p = exp2f(x[j] - mu);
       l += p;
-      p_smem[(2 * j + half) * kMaxG + head] = p;
+      p_smem[(j * kPer + lane / kL) * kMaxG + head] = p;
     }
     p_smem[kRows * kMaxG + head] = f;
     __syncwarp();
-    auto weights = [&](int row, float (&w)[GP]) {
-      const float* pp = p_smem + row * kMaxG;
-      if constexpr (GP >= 4) {
-#pragma unroll
-        for (int g = 0; g < GP; g += 4) {
-          const float4 t = *reinterpret_cast<const float4*>(pp + g);
-          w[g] = t.x;
-          w[g + 1] = t.y;
-          w[g + 2] = t.z;
-          w[g + 3] = t.w;
-        }
-      } else {
-#pragma unroll
-        for (int g = 0; g < GP; ++g) w[g] = pp[g];
-      }
-    };
     const char* vs = in.take();
     if (!vs) return;
     float w[GP];
-    weights(kRows, w);
+    weights(p_smem, kRows, w);
 #pragma unroll
-    for (int g = 0; g < GP; ++g)
-#pragma unroll
-      for (int i = 0; i < kD; ++i) o[g][i] *= w[g];
-#pragma unroll
-    for (int row = 0; row < kRows; ++row) {
-      if (row >= valid) break;  // rows behind the last hold anything
-      if (!(have >> (row / kGroup) & 1)) continue;
-      const float* vr = reinterpret_cast<const float*>(vs + row * DH * 4) + lane * kD;
-      float vx[kD];
-      if constexpr (kD == 4) {
-        const float4 t = *reinterpret_cast<const float4*>(vr);
-        vx[0] = t.x;
-        vx[1] = t.y;
-        vx[2] = t.z;
-        vx[3] = t.w;
-      } else {
-        const float2 t = *reinterpret_cast<const float2*>(vr);
-        vx[0] = t.x;
-        vx[1] = t.y;
+    for (int g = 0; g < GP; ++g) o[g] = make_float4(o[g].x * w[g], o[g].y * w[g], o[g].z * w[g], o[g].w * w[g]);
+    if (full) {
+#pragma unroll 8
+      for (int r = 0; r < kRows; r += 32 / kV) add_row(vs, p_smem, r + lane / kV, lane);
+    } else {
+#pragma unroll 1
+      for (int r = 0; r < kRows; r += 32 / kV) {
+        const int row = r + lane / kV;
+        if (row < valid && (have >> (row / kGroup) & 1)) add_row(vs, p_smem, row, lane);
       }
-      weights(row, w);
-#pragma unroll
-      for (int g = 0; g < GP; ++g)
-#pragma unroll
-        for (int i = 0; i < kD; ++i) o[g][i] = fmaf(w[g], vx[i], o[g][i]);
     }
     sm100::fence_async_smem();  // the weights were written by this thread, the next rows come by a bulk copy
     __syncwarp();
@@ -829,15 +826,51 @@ struct F32Rows {
     in.issue();
   }
 
+  __device__ __forceinline__ static void weights(const float* p_smem, int row, float (&w)[GP]) {
+    const float* pp = p_smem + row * kMaxG;
+    if constexpr (GP >= 4) {
+#pragma unroll
+      for (int g = 0; g < GP; g += 4) {
+        const float4 t = *reinterpret_cast<const float4*>(pp + g);
+        w[g] = t.x;
+        w[g + 1] = t.y;
+        w[g + 2] = t.z;
+        w[g + 3] = t.w;
+      }
+    } else {
+#pragma unroll
+      for (int g = 0; g < GP; ++g) w[g] = pp[g];
+    }
+  }
+  __device__ __forceinline__ void add_row(const char* vs, const float* p_smem, int row, int lane) {
+    const float4 v = *reinterpret_cast<const float4*>(vs + row * DH * 4 + lane % kV * 16);
+    float w[GP];
+    weights(p_smem, row, w);
+#pragma unroll
+    for (int g = 0; g < GP; ++g) {
+      o[g].x = fmaf(w[g], v.x, o[g].x);
+      o[g].y = fmaf(w[g], v.y, o[g].y);
+      o[g].z = fmaf(w[g], v.z, o[g].z);
+      o[g].w = fmaf(w[g], v.w, o[g].w);
+    }
+  }
+
   __device__ __forceinline__ void finish(Merge<DH, GP>& mg, int buf, int warp, int lane) {
-    l += __shfl_xor_sync(0xffffffffu, l, 16);
+#pragma unroll
+    for (int s = kL; s < 32; s <<= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
     const int head = head_of(lane);
     mg.m[buf][warp][head] = m;
     mg.l[buf][warp][head] = l;
 #pragma unroll
-    for (int g = 0; g < GP; ++g)
-#pragma unroll
-      for (int i = 0; i < kD; ++i) mg.o[buf][warp][g][lane * kD + i] = o[g][i];
+    for (int g = 0; g < GP; ++g) {
+      if constexpr (kV == 16) {
+        o[g].x += __shfl_xor_sync(0xffffffffu, o[g].x, 16);
+        o[g].y += __shfl_xor_sync(0xffffffffu, o[g].y, 16);
+        o[g].z += __shfl_xor_sync(0xffffffffu, o[g].z, 16);
+        o[g].w += __shfl_xor_sync(0xffffffffu, o[g].w, 16);
+      }
+      if (lane < kV) *reinterpret_cast<float4*>(&mg.o[buf][warp][g][lane * 4]) = o[g];
+    }
   }
 };
 
@@ -914,46 +947,48 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
 // Join the partial results.  CTA j looks at the cut between ranges j and j + 1:
 // where it falls inside a pair, that pair has np >= 2 parts and np - 1 such
 // cuts inside, and the CTA of cut i joins share i of the pair's G d_h outputs.
-// A thread loads its parts' (m, l, o) at once and folds them; threads of the
-// same outputs fold by a tree in shared memory (a fixed order: the result does
-// not depend on timing).  One round trip to L2 after the attention's end; the
-// search for the cut runs before it.
+// A warp takes cp words of four outputs, its lanes beyond those the parts in
+// turn: a lane loads its parts' (m, l, o) at once and folds them, then the
+// lanes of the same word fold (a fixed order: the result does not depend on
+// timing).  One round trip to L2 after the attention's end; the search for the
+// cut runs before it.
 template <int DH>
 __global__ void __launch_bounds__(kThreads) kv_join_kernel(const __grid_constant__ AttendArgs a) {
   __shared__ int sh_loc[kLocateWords];
-  __shared__ float2 sh_ml[kThreads];
-  __shared__ float4 sh_o[kThreads];
-  const int tid = threadIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Place at;
   bool empty;
   // the lengths were final before the first kernel passed its own wait
   const int c = blockIdx.x + 1;
   const Cut cut = locate(a, c, sh_loc, nullptr, at, empty);
+  int q0 = 0, q1 = 0, c0 = 0, np = 0, slot0 = 0, b = 0, h = 0;
+  if (c < cut.g && cut.start(c) != at.s) {
+    c0 = cut.range_of(at.s);
+    np = cut.range_of(at.s + units_of(at.len, a.unit_log) - 1) - c0 + 1;
+    const int cols = a.G * DH / 4, share = c - c0 - 1;
+    q0 = cols * share / (np - 1);
+    q1 = cols * (share + 1) / (np - 1);
+    // range c0's part of this pair is its first segment only where the range begins with the pair
+    slot0 = cut.start(c0) == at.s ? 0 : 1;
+    b = at.bh / a.H;
+    h = at.bh - b * a.H;
+  }
+  const int stride = kv_part_floats(a.G, DH);
+  int cp = 8;  // words per warp; as few as there are, so that more lanes share the parts
+  while (cp > 1 && cp >= 2 * (q1 - q0)) cp >>= 1;
+  const int groups = 32 / cp, grp = lane / cp;
   sm100::grid_dep_wait();
   sm100::grid_dep_launch();
   if (empty) {
     for (int e = blockIdx.x; e < a.BH; e += gridDim.x) {
       if (a.c.len(e) != 0) continue;
-      const int b = e / a.H, h = e - b * a.H;
-      for (int i = tid * 4; i < a.G * DH; i += kThreads * 4)
-        write_out<DH>(a, e, b, h, i / DH, i % DH, -INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f));
+      const int eb = e / a.H, eh = e - eb * a.H;
+      for (int i = threadIdx.x * 4; i < a.G * DH; i += kThreads * 4)
+        write_out<DH>(a, e, eb, eh, i / DH, i % DH, -INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f));
     }
   }
-  if (c >= cut.g || cut.start(c) == at.s) return;
-  const int c0 = cut.range_of(at.s), np = cut.range_of(at.s + units_of(at.len, a.unit_log) - 1) - c0 + 1;
-  const int stride = kv_part_floats(a.G, DH);
-  const int cols = a.G * DH / 4, share = c - c0 - 1;
-  const int q0 = cols * share / (np - 1), nq = cols * (share + 1) / (np - 1) - q0;
-  if (nq == 0) return;
-  int cp = 1;  // threads across the outputs; the rest of them across the parts
-  while (cp < nq && cp < kThreads) cp <<= 1;
-  const int groups = kThreads / cp, grp = tid / cp;
-  const int b = at.bh / a.H, h = at.bh - b * a.H;
-  // range c0's part of this pair is its first segment only where the range begins with the pair
-  const int slot0 = cut.start(c0) == at.s ? 0 : 1;
-  for (int qb = 0; qb < nq; qb += cp) {
-    const int q = q0 + qb + tid % cp;
-    const int g = min(q * 4 / DH, a.G - 1);
+  for (int qb = q0 + warp * cp; qb < q1; qb += kWarps * cp) {
+    const int q = min(qb + lane % cp, q1 - 1), g = q / (DH / 4);
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     auto fold = [&](float m2, float l2, float4 o2) {
@@ -966,27 +1001,19 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(const __grid_constant
       o.z = fmaf(o.z, f, o2.z * f2);
       o.w = fmaf(o.w, f, o2.w * f2);
     };
-    if (q < q0 + nq) {
 #pragma unroll 4
-      for (int i = grp; i < np; i += groups) {
-        const float* part = a.part + ((c0 + i) * 2 + (i == 0 ? slot0 : 0)) * (int64_t)stride;
-        const float pm = __ldcg(part + a.G * DH + g), pl = __ldcg(part + a.G * DH + kMaxG + g);
-        fold(pm, pl, __ldcg(reinterpret_cast<const float4*>(part) + q));
-      }
+    for (int i = grp; i < np; i += groups) {
+      const float* part = a.part + ((c0 + i) * 2 + (i == 0 ? slot0 : 0)) * (int64_t)stride;
+      const float pm = __ldcg(part + a.G * DH + g), pl = __ldcg(part + a.G * DH + kMaxG + g);
+      fold(pm, pl, __ldcg(reinterpret_cast<const float4*>(part) + q));
     }
-    sh_ml[tid] = make_float2(m, l);
-    sh_o[tid] = o;
-    for (int n = groups >> 1; n > 0; n >>= 1) {
-      __syncthreads();
-      if (grp < n) {
-        const float2 v = sh_ml[tid + n * cp];
-        fold(v.x, v.y, sh_o[tid + n * cp]);
-        sh_ml[tid] = make_float2(m, l);
-        sh_o[tid] = o;
-      }
+    for (int s = cp; s < 32; s <<= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, s), l2 = __shfl_xor_sync(0xffffffffu, l, s);
+      const float4 o2 = make_float4(__shfl_xor_sync(0xffffffffu, o.x, s), __shfl_xor_sync(0xffffffffu, o.y, s),
+                                    __shfl_xor_sync(0xffffffffu, o.z, s), __shfl_xor_sync(0xffffffffu, o.w, s));
+      fold(m2, l2, o2);
     }
-    if (grp == 0 && q < q0 + nq) write_out<DH>(a, at.bh, b, h, g, q * 4 % DH, m, l, o);
-    __syncthreads();
+    if (grp == 0 && qb + lane < q1) write_out<DH>(a, at.bh, b, h, g, q * 4 % DH, m, l, o);
   }
 }
 
@@ -995,28 +1022,53 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(const __grid_constant
 // it reads and writes (4 G + 8 bytes a row).
 constexpr int kWeightRows = 4 * kThreads;
 
+// V: logits per load, the largest of 4, 2, 1 that divides G.
+template <int V>
 __global__ void __launch_bounds__(kThreads) kv_weights_kernel(const __grid_constant__ AttendArgs a, int chunks) {
   const int bh = blockIdx.x / chunks, r0 = (blockIdx.x - bh * chunks) * kWeightRows + threadIdx.x;
   const int len = a.c.len(bh);  // final before the first kernel of the call passed its wait
   sm100::grid_dep_wait();
   if (r0 >= len) return;
-  float L[kMaxG];
-#pragma unroll
-  for (int g = 0; g < kMaxG; ++g) L[g] = g < a.G ? __ldcg(a.lse2 + (int64_t)bh * a.G + g) : -INFINITY;
+  const int n = a.G / V;
+  const float* lp = a.lse2 + (int64_t)bh * a.G;
   const float* x = a.logits + ((int64_t)bh * a.c.max_len + r0) * a.G;
   float* w = a.w + bh * a.cap + r0;
-  float p[4];
+  float old[4], p[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    p[i] = 0.f;
-    if (r0 + i * kThreads < len)
+  for (int i = 0; i < 4; ++i) old[i] = r0 + i * kThreads < len ? __ldcg(w + i * kThreads) : 0.f;
 #pragma unroll
-      for (int g = 0; g < kMaxG; ++g)
-        if (g < a.G && L[g] != -INFINITY) p[i] += exp2f(__ldcg(x + (int64_t)i * kThreads * a.G + g) - L[g]);
+  for (int k = 0; k < kMaxG / V; ++k) {
+    if (k >= n) break;
+    float v[4][V];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float* xp = x + (int64_t)i * kThreads * a.G + k * V;
+      const bool in = r0 + i * kThreads < len;
+      if constexpr (V == 4) {
+        const float4 t = in ? __ldcg(reinterpret_cast<const float4*>(xp)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[i][0] = t.x;
+        v[i][1] = t.y;
+        v[i][2] = t.z;
+        v[i][3] = t.w;
+      } else if constexpr (V == 2) {
+        const float2 t = in ? __ldcg(reinterpret_cast<const float2*>(xp)) : make_float2(0.f, 0.f);
+        v[i][0] = t.x;
+        v[i][1] = t.y;
+      } else {
+        v[i][0] = in ? __ldcg(xp) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < V; ++g) {
+      const float L = __ldcg(lp + k * V + g);
+      if (L != -INFINITY)  // else no row of the pair counts for this head
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] += exp2f(v[i][g] - L);
+    }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (r0 + i * kThreads < len) w[i * kThreads] = fmaf(a.decay, w[i * kThreads], p[i]);
+    if (r0 + i * kThreads < len) w[i * kThreads] = fmaf(a.decay, old[i], p[i]);
 }
 
 // Let a kernel use `smem` bytes of dynamic shared memory on the current device;
@@ -1027,7 +1079,9 @@ cudaError_t allow_smem(const void* kern, size_t smem, std::atomic<uint64_t>& rea
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the whole L1 as shared memory for all kernels of a call: an SM need not be reconfigured between them
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }
@@ -1045,14 +1099,18 @@ cudaError_t launch_t(const Plan& p, const AttendArgs& a, int grid, cudaStream_t 
     e = launch_pdl(kern, grid, kThreads, smem, st, a);
   }
   if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> ready_join{0};
+  e = allow_smem((const void*)kv_join_kernel<DH>, 0, ready_join);
+  if (e != cudaSuccess) return e;
   {
     ProfScope ps(p, st, KID_KV_JOIN);
     e = launch_pdl(kv_join_kernel<DH>, grid, kThreads, 0, st, a);
   }
   if (e != cudaSuccess || !a.w) return e;
   const int chunks = (int)ceil_div64(a.c.max_len, kWeightRows);
+  auto weights = a.G % 4 == 0 ? kv_weights_kernel<4> : a.G % 2 == 0 ? kv_weights_kernel<2> : kv_weights_kernel<1>;
   ProfScope ps(p, st, KID_KV_WEIGHTS);
-  return launch_pdl(kv_weights_kernel, (unsigned)a.BH * chunks, kThreads, 0, st, a, chunks);
+  return launch_pdl(weights, (unsigned)a.BH * chunks, kThreads, 0, st, a, chunks);
 }
 
 template <int DH>
