@@ -233,6 +233,14 @@ __device__ __forceinline__ void finish_segments(const AttendArgs& a, const Merge
   }
 }
 
+// 2^x by the special-function unit alone (relative error 2^-22, results below
+// 2^-126 are 0).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // ---- the rows' way into shared memory
 // A warp takes every eighth unit of its CTA's range through a ring of three
 // 8 KB slots of its own, K rows and V rows in turn: lane 0 issues bulk copies
@@ -389,16 +397,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// z becomes NaN in a half where v's is infinite or NaN, else keeps its value.
-__device__ __forceinline__ void note_nonfinite(uint32_t& z, uint32_t v) {
-  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(z) : "r"(v), "r"(0u));
-}
-// v with its infinite and NaN halves zero
-__device__ __forceinline__ uint32_t finite_halves(uint32_t v) {
-  const uint32_t t = (v & 0x7f807f80u) + 0x00800080u;  // bit 15 of a half: its exponent is all ones
-  return v & ~((t >> 15 & 0x00010001u) * 0xffffu);
-}
-
 // bfloat16 rows on the tensor cores, a unit (32 or 64 rows) a step, in groups
 // of 16.  Lane (gr, t) = (lane / 4, lane % 4).  Rows are the M side of both
 // products and the pair's query heads (at most 8, zero beyond G) the N side, so
@@ -414,10 +412,9 @@ __device__ __forceinline__ uint32_t finite_halves(uint32_t v) {
 //    into the columns 4 .. 7 of the first one's product, and with GP = 2 all
 //    three into one product: queries repeat over the columns, so that every
 //    lane has the weights at hand, and the columns of a head are added up at
-//    the segment's end.  An infinite V element must meet the first term only
-//    (the others may be zero or negative): where a group has any, the terms
-//    take V with such elements zeroed and one more product adds them, times the
-//    first term.
+//    the segment's end.  An infinite V element would meet the other terms too,
+//    which may be zero or negative: a warp whose sums are not finite at the
+//    segment's end computes its rows again on the CUDA cores (plain_rows).
 //  - A step's products go into zeroed accumulators that are then added to the
 //    running ones in float32: the tensor core's own additions may truncate,
 //    which over thousands of steps would bias the sums.
@@ -512,17 +509,17 @@ struct Bf16Rows {
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
       const float mu = mx == -INFINITY ? 0.f : mx;
-      f[c] = exp2f(m[c] - mu);
+      f[c] = ex2(m[c] - mu);
       m[c] = mx;
       l[c] *= f[c];
 #pragma unroll
       for (int n = 0; n < kG; ++n) {
-        x[n][c] = exp2f(x[n][c] - mu);
-        x[n][c + 2] = exp2f(x[n][c + 2] - mu);
+        x[n][c] = ex2(x[n][c] - mu);
+        x[n][c + 2] = ex2(x[n][c + 2] - mu);
         l[c] += x[n][c] + x[n][c + 2];
       }
     }
-    uint32_t p1[kG][2], pb[kG][kTerms][2];  // the first term, not yet transposed; the products' P
+    uint32_t pb[kG][kTerms][2];
 #pragma unroll
     for (int n = 0; n < kG; ++n)
 #pragma unroll
@@ -534,7 +531,6 @@ struct Bf16Rows {
           x[n][2 * hf] -= lo_f(w[s]);
           x[n][2 * hf + 1] -= hi_f(w[s]);
         }
-        p1[n][hf] = w[0];
         if constexpr (GP == 8) {
 #pragma unroll
           for (int s = 0; s < 3; ++s) pb[n][s][hf] = transpose8(w[s]);
@@ -567,21 +563,7 @@ struct Bf16Rows {
         __syncwarp();
         in.issue();
       }
-      uint32_t nz[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int w = 0; w < kH; ++w)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          note_nonfinite(nz[0], v[w][i].x);
-          note_nonfinite(nz[1], v[w][i].y);
-          note_nonfinite(nz[2], v[w][i].z);
-          note_nonfinite(nz[3], v[w][i].w);
-        }
-      // the halves are zero or NaN
-      if (!__any_sync(0xffffffffu, ((nz[0] | nz[1] | nz[2] | nz[3]) & 0x7fff7fffu) != 0u))
-        outputs<false>(c, v, p1[n], pb[n]);
-      else
-        outputs<true>(c, v, p1[n], pb[n]);
+      outputs(c, v, pb[n]);
     }
 #pragma unroll
     for (int j = 0; j < kM; ++j)
@@ -591,14 +573,7 @@ struct Bf16Rows {
 
   // C += V^T P for one group, four M tiles at a time, so that their chains of
   // products overlap.
-  template <bool kOdd>
-  __device__ __forceinline__ void outputs(float (&c)[kM][4], const uint4 (&v)[kH][4], const uint32_t (&p1)[2],
-                                          const uint32_t (&pb)[kTerms][2]) {
-    uint32_t ph[2] = {0u, 0u};
-    if (kOdd) {
-      ph[0] = transpose8(p1[0]);
-      ph[1] = transpose8(p1[1]);
-    }
+  __device__ __forceinline__ void outputs(float (&c)[kM][4], const uint4 (&v)[kH][4], const uint32_t (&pb)[kTerms][2]) {
 #pragma unroll
     for (int j0 = 0; j0 < kM; j0 += 4) {
       uint32_t av[4][4];
@@ -616,19 +591,6 @@ struct Bf16Rows {
           av[jj][i] = __byte_perm(ra[word], rb[word], high ? 0x7632 : 0x5410);
         }
       }
-      if (kOdd) {
-#pragma unroll
-        for (int jj = 0; jj < 4; ++jj) {
-          uint32_t od[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t fin = finite_halves(av[jj][i]);
-            od[i] = av[jj][i] ^ fin;  // the infinite and NaN halves
-            av[jj][i] = fin;
-          }
-          mma_bf16(c[j0 + jj], od[0], od[1], od[2], od[3], ph[0], ph[1]);
-        }
-      }
 #pragma unroll
       for (int s = kTerms - 1; s >= 0; --s)
 #pragma unroll
@@ -637,8 +599,15 @@ struct Bf16Rows {
     }
   }
 
-  __device__ __forceinline__ void finish(Merge<DH, GP>& mg, int buf, int warp, int lane) {
+  // Leave the warp's result; false where it is not finite (it is then computed another way).
+  __device__ __forceinline__ bool finish(Merge<DH, GP>& mg, int buf, int warp, int lane) {
     const int gr = lane >> 2, t = lane & 3;
+    float z = 0.f;  // 0, or NaN
+#pragma unroll
+    for (int j = 0; j < kM; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z = fmaf(o[j][i], 0.f, z);
+    if (__any_sync(0xffffffffu, z != 0.f)) return false;
     // add up the columns of a head
     if constexpr (GP < 8) {
 #pragma unroll
@@ -655,7 +624,7 @@ struct Bf16Rows {
       l[c] += __shfl_xor_sync(0xffffffffu, l[c], 8);
       l[c] += __shfl_xor_sync(0xffffffffu, l[c], 16);
     }
-    if (2 * t >= GP) return;
+    if (2 * t >= GP) return true;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       if (gr == 0) {
@@ -676,6 +645,7 @@ struct Bf16Rows {
           *reinterpret_cast<float4*>(op + 2 * j) = make_float4(o[j][c], o[j][2 + c], o[j + 1][c], o[j + 1][2 + c]);
       }
     }
+    return true;
   }
 };
 
@@ -792,13 +762,13 @@ struct F32Rows {
 #pragma unroll
     for (int s = kL; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
     const float mu = mx == -INFINITY ? 0.f : mx;
-    const float f = exp2f(m - mu);
+    const float f = ex2(m - mu);
     m = mx;
     l *= f;
     __syncwarp();  // every lane has read its K rows
 #pragma unroll
     for (int j = 0; j < kPasses; ++j) {
-      const float p = exp2f(x[j] - mu);
+      const float p = ex2(x[j] - mu);
       l += p;
       p_smem[(j * kPer + lane / kL) * kMaxG + head] = p;
     }
@@ -855,7 +825,7 @@ struct F32Rows {
     }
   }
 
-  __device__ __forceinline__ void finish(Merge<DH, GP>& mg, int buf, int warp, int lane) {
+  __device__ __forceinline__ bool finish(Merge<DH, GP>& mg, int buf, int warp, int lane) {
 #pragma unroll
     for (int s = kL; s < 32; s <<= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
     const int head = head_of(lane);
@@ -871,8 +841,50 @@ struct F32Rows {
       }
       if (lane < kV) *reinterpret_cast<float4*>(&mg.o[buf][warp][g][lane * 4]) = o[g];
     }
+    return true;
   }
 };
+
+// A warp's units u, u + kWarps, .. < ue of a pair (at), computed row by row in
+// float32 from global memory, for sums that an infinity or a NaN among the rows
+// made worthless: every product is then one of a weight and a value, as in the
+// formula.
+template <int DH, int GP>
+__device__ __noinline__ void plain_rows(const AttendArgs& a, Merge<DH, GP>& mg, int buf, Place at, int u, int ue,
+                                        int warp, int lane) {
+  constexpr int kN = DH / 32;
+  const int b = at.bh / a.H, h = at.bh - b * a.H;
+  for (int g = 0; g < GP; ++g) {
+    float q[kN], o[kN], m = -INFINITY, l = 0.f;
+    const auto* qp = static_cast<const __nv_bfloat16*>(a.q) + b * a.qsb + (int64_t)(h * a.G + g) * a.qsh;
+    for (int i = 0; i < kN; ++i) {
+      q[i] = g < a.G ? to_f(qp[i * 32 + lane]) : 0.f;
+      o[i] = 0.f;
+    }
+    for (int n = u; g < a.G && n < ue; n += kWarps) {
+      const int r0 = (n - at.s) << a.unit_log, r1 = min(at.len, r0 + (1 << a.unit_log));
+      for (int r = r0; r < r1; ++r) {
+        const int64_t row = a.c.row(at.bh, r);
+        if (row < 0) continue;
+        const auto* kr = reinterpret_cast<const __nv_bfloat16*>(a.c.k) + row * DH;
+        const auto* vr = reinterpret_cast<const __nv_bfloat16*>(a.c.v) + row * DH;
+        float x = 0.f;
+        for (int i = 0; i < kN; ++i) x = fmaf(q[i], to_f(kr[i * 32 + lane]), x);
+        x = warp_sum(x) * a.scale2;
+        const float mx = fmaxf(m, x), mu = mx == -INFINITY ? 0.f : mx;
+        const float f = exp2f(m - mu), p = exp2f(x - mu);
+        m = mx;
+        l = fmaf(l, f, p);
+        for (int i = 0; i < kN; ++i) o[i] = fmaf(o[i], f, p * to_f(vr[i * 32 + lane]));
+      }
+    }
+    if (lane == 0) {
+      mg.m[buf][warp][g] = m;
+      mg.l[buf][warp][g] = l;
+    }
+    for (int i = 0; i < kN; ++i) mg.o[buf][warp][g][i * 32 + lane] = o[i];
+  }
+}
 
 __device__ __forceinline__ void init_ring(RingSmem& ring, int warp, int lane) {
   if (lane == 0) {
@@ -924,7 +936,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
       float* xl = a.w ? a.logits + ((int64_t)at.bh * a.c.max_len + r) * a.G : nullptr;
       rows.step(a, in, min(at.len - r, kRows), xl, lane);
     }
-    rows.finish(sm.merge, held, warp, lane);
+    if (!rows.finish(sm.merge, held, warp, lane))
+      plain_rows(a, sm.merge, held, at, u + ((u_first + warp - u) & (kWarps - 1)), ue, warp, lane);
     if (threadIdx.x == 0) {
       sm.merge.bh[held] = at.bh;
       sm.merge.slot[held] = u == at.s && ue == at.s + ub ? -1 : u == u_first ? 0 : 1;
