@@ -3,6 +3,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 #include "internal.h"
@@ -26,6 +27,45 @@ cudaError_t launch_pdl(void (*kern)(P...), unsigned grid, unsigned threads, size
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
+// The same for a grid of clusters of `cluster` CTAs.
+template <typename... P, typename... A>
+cudaError_t launch_pdl_cluster(void (*kern)(P...), unsigned grid, unsigned threads, unsigned cluster, size_t smem,
+                               cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
+// Let a kernel use `smem` bytes of dynamic shared memory (and clusters of more
+// than eight CTAs) on the current device; `ready` keeps the devices, of the
+// first 64, that have it already.
+inline cudaError_t allow_smem(const void* kern, size_t smem, std::atomic<uint64_t>& ready, bool large_cluster = false) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  if (smem) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the whole L1 as shared memory for all kernels of a call: an SM need not be reconfigured between them
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+  if (e == cudaSuccess && large_cluster)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 template <typename T> __device__ __forceinline__ float to_f(T v);

@@ -1084,21 +1084,6 @@ __global__ void __launch_bounds__(kThreads) kv_weights_kernel(const __grid_const
     if (r0 + i * kThreads < len) w[i * kThreads] = fmaf(a.decay, old[i], p[i]);
 }
 
-// Let a kernel use `smem` bytes of dynamic shared memory on the current device;
-// `ready` keeps the devices (of the first 64) that have it already.
-cudaError_t allow_smem(const void* kern, size_t smem, std::atomic<uint64_t>& ready) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  if (smem) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  // the whole L1 as shared memory for all kernels of a call: an SM need not be reconfigured between them
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
-  return e;
-}
-
 template <int DH, typename Rows>
 cudaError_t launch_t(const Plan& p, const AttendArgs& a, int grid, cudaStream_t st) {
   auto kern = kv_attend_kernel<DH, Rows>;

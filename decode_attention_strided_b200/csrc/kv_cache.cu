@@ -1,24 +1,30 @@
 // kv_cache.cu -- the plain paged cache's rows: appending tokens, and evicting
 // the rows with the least accumulated attention weight.
 #include <algorithm>
+#include <atomic>
+
+#include <cooperative_groups.h>
 
 #include "common.cuh"
+#include "sm100.cuh"
 
 namespace dkv {
 
 namespace {
 
 // ---- append
-// One 16-byte word of one new row per thread and step: the rows of a pair are
-// its K row's words and then its V row's.  Pure copying: bound by the rows read
-// and written once each.
+// A warp copies kAppendRows new rows of a pair: a lane looks up where one row
+// goes, then the warp loads all rows' 16-byte words (K and V) before it stores
+// the first.  Pure copying: bound by the rows read and written once each.
+constexpr int kAppendRows = 8;
+constexpr int kAppendWarps = 8;
+
 struct AppendArgs {
   KvView c;
-  int64_t BH;
-  int H, n_new, words;  // words: 16-byte words of one K row
+  int H, n_new, chunks;  // chunks: CTAs per pair
   const char* K;
   const char* V;
-  int64_t sb, sh, st;   // byte strides
+  int64_t sb, sh, st;    // byte strides
   const int32_t* n_tokens;
   const int32_t* first_pos;
   float* w;
@@ -27,49 +33,73 @@ struct AppendArgs {
   const float* tok_w;
 };
 
-__global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
-  const int per_row = 2 * a.words;  // a power of two, at most 64
-  const int rows_blk = 256 / per_row;
-  const int64_t chunks = (a.n_new + rows_blk - 1) / rows_blk;
-  const int t0 = threadIdx.x / per_row, word = threadIdx.x % per_row;
-  for (int64_t i = blockIdx.x; i < a.BH * chunks; i += gridDim.x) {
-    const int64_t bh = i / chunks;
-    const int64_t t = (i % chunks) * rows_blk + t0;
-    const int64_t b = bh / a.H;
-    const int h = (int)(bh % a.H);
-    const int len = a.c.len(bh), raw = a.c.lens[bh];
-    const int nb = a.n_tokens ? a.n_tokens[b] : a.n_new;
-    if (raw != len || nb < 0 || nb > a.n_new || nb > len) {
-      if (threadIdx.x == 0) a.c.report((uint32_t)nb);
-      continue;
-    }
-    if (t >= nb) continue;
-    const int r = len - nb + (int)t;
-    if (word == 0) {
-      if (a.w) a.w[bh * a.cap + r] = a.tok_w ? a.tok_w[bh * a.n_new + t] : 0.f;
-      if (a.pos) a.pos[bh * a.cap + r] = a.first_pos[b] + (int)t;
-    }
-    const int64_t row = a.c.row(bh, r);
-    if (row < 0) continue;
-    const bool is_v = word >= a.words;
-    const int wd = is_v ? word - a.words : word;
-    const char* src = (is_v ? a.V : a.K) + b * a.sb + h * a.sh + t * a.st;
-    char* dst = (is_v ? a.c.v : a.c.k) + row * a.words * 16;
-    reinterpret_cast<uint4*>(dst)[wd] = reinterpret_cast<const uint4*>(src)[wd];
+// kWords: 16-byte words of one row's K and V together (16, 32 or 64).
+template <int kWords>
+__global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+  const int bh = blockIdx.x / a.chunks;
+  const int b = bh / a.H, h = bh - b * a.H;
+  const int lane = threadIdx.x & 31;
+  const int t0 = ((blockIdx.x - bh * a.chunks) * kAppendWarps + (threadIdx.x >> 5)) * kAppendRows;
+  sm100::grid_dep_wait();
+  const int raw = a.c.raw_len(bh), len = a.c.checked(raw);
+  const int nb = a.n_tokens ? __ldcg(a.n_tokens + b) : a.n_new;
+  if (raw != len || nb < 0 || nb > a.n_new || nb > len) {
+    if (threadIdx.x == 0) a.c.report((uint32_t)(raw != len ? raw : nb));
+    return;
   }
+  const int rows = min(kAppendRows, nb - t0);
+  if (rows <= 0) return;
+  int64_t row = -1;
+  if (lane < rows) {
+    const int t = t0 + lane, r = len - nb + t;
+    row = a.c.row(bh, r);
+    if (a.w) a.w[bh * a.cap + r] = a.tok_w ? a.tok_w[(int64_t)bh * a.n_new + t] : 0.f;
+    if (a.pos) a.pos[bh * a.cap + r] = a.first_pos[b] + t;
+  }
+  __syncwarp();
+  constexpr int kHalf = kWords / 2;
+  constexpr int kLoads = kAppendRows * kWords / 32;
+  const int64_t src = b * a.sb + h * a.sh + (int64_t)t0 * a.st;
+  uint4 v[kLoads];
+  char* dst[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int k = (i * 32 + lane) / kWords, word = lane % kWords + (kWords == 64 ? (i & 1) * 32 : 0);
+    const int64_t to = __shfl_sync(0xffffffffu, row, k);
+    const bool is_v = word >= kHalf;
+    const int wd = is_v ? word - kHalf : word;
+    dst[i] = k < rows && to >= 0 ? (is_v ? a.c.v : a.c.k) + to * (kHalf * 16) + wd * 16 : nullptr;
+    if (dst[i]) v[i] = __ldcg(reinterpret_cast<const uint4*>((is_v ? a.V : a.K) + src + k * a.st) + wd);
+  }
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i)
+    if (dst[i]) *reinterpret_cast<uint4*>(dst[i]) = v[i];
 }
 
 // ---- evict
-// Each pair: the m-th largest key of its n rows by a radix select (most
-// significant byte first), the rows above it and the first rows equal to it
-// are kept; a scan in row order numbers the dropped rows below m (holes) and
-// the kept rows at or past m (movers), of which there are equally many: mover
-// i goes to hole i.  A second kernel moves the rows.
-constexpr int kSelThreads = 1024;
+// A cluster of CTAs per pair, each with a run of its rows.  Weights become
+// integer keys that order like them (kept in shared memory where they fit),
+// and the m-th largest key is found by narrowing a range of keys: 1024 equal
+// bins over it, counted per CTA and added up over the cluster through
+// distributed shared memory, until the bin that holds the m-th key is kept
+// whole or holds one key only; two rounds as a rule, three or four at most.
+// Rows above the threshold and the first of those equal to it are kept; a scan
+// in row order numbers the dropped rows below m (holes) and the kept rows at or
+// past m (movers), of which there are equally many: mover i goes to hole i.
+// Bound by its chain of block and cluster barriers: the keys are read once.  A
+// second kernel moves the rows, spread over the whole GPU whatever the pairs'
+// shares: bound by the rows read and written.
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBinBits = 10;
+constexpr int kBins = 1 << kBinBits;
+constexpr int kRun = 16;              // consecutive rows per thread in the scan
+constexpr int kSelCached = 24 * 1024; // rows per CTA whose keys shared memory holds (two CTAs per SM)
+constexpr int kMaxCluster = 16;
 
 struct EvictArgs {
   KvView c;
-  int64_t BH;
+  int BH, cluster;
   const int32_t* budget;
   int n_first, n_recent;
   const float* w;
@@ -82,10 +112,9 @@ struct EvictArgs {
   int32_t* hole;   // [BH][half]
   int32_t* move;   // [BH][half]
   int64_t half;
-  int words;       // 16-byte words of one K row
 };
 
-constexpr uint32_t kGuarded = 0xffffffffu;
+constexpr uint32_t kGuarded = 0xffffffffu;  // above every weight's key
 
 // Weight as a key that orders like it: NaN lowest (0), -0 as +0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -94,7 +123,8 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix of v over the block; total in `all`.
+// Exclusive prefix of v over the block; total in `all`.  sh: 32 words, in use
+// until the next barrier.
 __device__ __forceinline__ int block_scan(int v, int& all, int* sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int inc = v;
@@ -106,132 +136,340 @@ __device__ __forceinline__ int block_scan(int v, int& all, int* sh) {
   __syncthreads();
   if (lane == 31) sh[warp] = inc;
   __syncthreads();
-  int t = sh[lane], ti = t;
+  const int t = lane < kSelWarps ? sh[lane] : 0;
+  int ti = t;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
+  for (int o = 1; o < kSelWarps; o <<= 1) {
     const int u = __shfl_up_sync(0xffffffffu, ti, o);
     if (lane >= o) ti += u;
   }
-  all = __shfl_sync(0xffffffffu, ti, 31);
+  all = __shfl_sync(0xffffffffu, ti, kSelWarps - 1);
   return __shfl_sync(0xffffffffu, ti - t, warp) + inc - v;
 }
 
-__global__ void __launch_bounds__(kSelThreads) kv_select_kernel(EvictArgs a) {
-  __shared__ int sh[32];
-  __shared__ int hist[256];
-  __shared__ uint32_t sh_prefix;
-  __shared__ int sh_need;
-  const int64_t bh = blockIdx.x;
-  const int tid = threadIdx.x;
-  const int raw = a.c.lens[bh], n = a.c.len(bh), budget = a.budget[bh];
+// What a CTA tells the others of its cluster.
+struct SelExchange {
+  uint32_t kmin, kmax;
+  int last, bad;      // largest position; a page out of range
+  int holes, movers;
+};
+
+struct SelSmem {
+  int hist[2][kBins + 1];        // the last bin: guarded rows
+  SelExchange from[kMaxCluster]; // written by the CTAs of the cluster
+  int scan[32];
+  uint32_t rmin[kSelWarps], rmax[kSelWarps];
+  int rlast[kSelWarps];
+  int found, found_count, found_above;
+};
+
+__global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_constant__ EvictArgs a, int cached) {
+  namespace cg = cooperative_groups;
+  extern __shared__ uint32_t keys[];  // row lo + i at i + i / kRun: a thread's run meets all banks
+  __shared__ SelSmem sm;
+  const cg::cluster_group cl = cg::this_cluster();
+  const int C = a.cluster, rank = C == 1 ? 0 : (int)cl.block_rank();
+  const int bh = blockIdx.x / C;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  sm100::grid_dep_wait();
+  sm100::grid_dep_launch();
+  if (C > 1) cg::cluster_group::barrier_arrive();  // the others' shared memory is there from the wait on
+  const int raw = a.c.raw_len(bh), n = a.c.checked(raw), budget = a.budget[bh];
   int m = min(n, max(budget, a.n_first + a.n_recent));
-  int bad = 0;
-  for (int l = tid; l < ((n - 1) >> a.c.page_log) + 1 && n > 0; l += kSelThreads)
-    bad |= a.c.row(bh, l << a.c.page_log) < 0;
-  bad = __syncthreads_or(bad);
-  if (tid == 0 && (raw != n || budget < 0)) a.c.report((uint32_t)(raw != n ? raw : budget));
-  if (bad || budget < 0) m = n;
+  if (rank == 0 && tid == 0 && (raw != n || budget < 0)) a.c.report((uint32_t)(raw != n ? raw : budget));
   const float* w = a.w + bh * a.cap;
   const int32_t* pos = a.pos + bh * a.cap;
-  float* wo = a.w_out + bh * a.cap;
-  int32_t* po = a.pos_out + bh * a.cap;
-  int cnt = 0;
-  if (m == n) {
-    for (int r = tid; r < n; r += kSelThreads) {
-      wo[r] = w[r];
-      po[r] = pos[r];
-    }
-  } else if (m > 0) {
-    int last = INT32_MIN;
-    for (int r = tid; r < n; r += kSelThreads) last = max(last, pos[r]);
-    last = __reduce_max_sync(0xffffffffu, last);
-    if ((tid & 31) == 0) sh[tid >> 5] = last;
-    __syncthreads();
-    last = __reduce_max_sync(0xffffffffu, sh[tid & 31]);
-    const int64_t from = (int64_t)last - a.n_recent;
-    auto key = [&](int r) {
-      const int p = pos[r];
-      return p < a.n_first || p > from ? kGuarded : weight_key(w[r]);
-    };
-    uint32_t prefix = 0;
-    int need = m;  // rows still to keep among the keys with this prefix
-    for (int shift = 24; shift >= 0; shift -= 8) {
+  const int run = ((n + C - 1) / C + kRun - 1) / kRun * kRun;  // rows per CTA
+  const int lo = min(n, rank * run), hi = min(n, lo + run);
+  auto sync = [&] {
+    if (C == 1)
       __syncthreads();
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-      for (int r = tid; r < n; r += kSelThreads) {
-        const uint32_t k = key(r);
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
-      }
-      __syncthreads();
-      if (tid == 0) {
-        int left = need, d = 255;
-        for (; d > 0 && hist[d] < left; --d) left -= hist[d];
-        sh_prefix = prefix | ((uint32_t)d << shift);
-        sh_need = left;
-      }
-      __syncthreads();
-      prefix = sh_prefix;
-      need = sh_need;
-    }
-    // keep: keys above the threshold, and its first `need` rows
-    int eq_before = 0, hole_before = 0, move_before = 0;
-    for (int r0 = 0; r0 < n; r0 += kSelThreads) {
-      const int r = r0 + tid;
-      const uint32_t k = r < n ? key(r) : 0u;
-      const int eq = r < n && k == prefix;
-      int all;
-      const int eq_rank = eq_before + block_scan(eq, all, sh);
-      eq_before += all;
-      const bool keep = r < n && (k > prefix || (eq && eq_rank < need));
-      const int is_hole = r < m && !keep, is_move = r >= m && keep;
-      const int rank = block_scan(is_hole | (is_move << 16), all, sh);
-      if (is_hole) a.hole[bh * a.half + hole_before + (rank & 0xffff)] = r;
-      if (is_move) a.move[bh * a.half + move_before + (rank >> 16)] = r;
-      hole_before += all & 0xffff;
-      move_before += all >> 16;
-      if (keep && r < m) {
-        wo[r] = w[r];
-        po[r] = pos[r];
-      }
-    }
-    cnt = hole_before;
+    else
+      cl.sync();
+  };
+  // ---- keys of this CTA's rows, their range, the largest position, and the pages
+  uint32_t kmin = 0xffffffffu, kmax = 0u;
+  int last = INT32_MIN, bad = 0;
+#pragma unroll 4
+  for (int r = lo + tid; r < hi; r += kSelThreads) {
+    const uint32_t k = weight_key(__ldcg(w + r));
+    if (cached) keys[r - lo + (r - lo) / kRun] = k;
+    kmin = min(kmin, k);
+    kmax = max(kmax, k);
+    last = max(last, __ldcg(pos + r));
   }
-  __syncthreads();
-  if (tid == 0) {
-    a.count[bh] = cnt;
+  // the pages of the rows this CTA starts with
+  for (int r = ((lo >> a.c.page_log) + tid) << a.c.page_log; r < hi; r += kSelThreads << a.c.page_log)
+    bad |= a.c.row(bh, r) < 0;
+  kmin = __reduce_min_sync(0xffffffffu, kmin);
+  kmax = __reduce_max_sync(0xffffffffu, kmax);
+  last = __reduce_max_sync(0xffffffffu, last);
+  if (lane == 0) {
+    sm.rmin[warp] = kmin;
+    sm.rmax[warp] = kmax;
+    sm.rlast[warp] = last;
+  }
+  bad = __syncthreads_or(bad);
+  if (C > 1) cg::cluster_group::barrier_wait();
+  if (warp == 0) {
+    const int s = lane % kSelWarps;
+    kmin = __reduce_min_sync(0xffffffffu, sm.rmin[s]);
+    kmax = __reduce_max_sync(0xffffffffu, sm.rmax[s]);
+    last = __reduce_max_sync(0xffffffffu, sm.rlast[s]);
+    if (lane < C) {
+      SelExchange* to = C == 1 ? &sm.from[0] : cl.map_shared_rank(&sm.from[rank], lane);
+      to->kmin = kmin;
+      to->kmax = kmax;
+      to->last = last;
+      to->bad = bad;
+    }
+  }
+  sync();
+  for (int i = 0; i < C; ++i) {
+    kmin = i == 0 ? sm.from[0].kmin : min(kmin, sm.from[i].kmin);
+    kmax = i == 0 ? sm.from[0].kmax : max(kmax, sm.from[i].kmax);
+    last = i == 0 ? sm.from[0].last : max(last, sm.from[i].last);
+    bad |= sm.from[i].bad;
+  }
+  if (bad || budget < 0) m = n;
+  // rows below m start out as themselves; the move writes over the holes
+  if (a.w_out != a.w)
+    for (int r = lo + tid; r < min(hi, m); r += kSelThreads) a.w_out[bh * a.cap + r] = w[r];
+  if (a.pos_out != a.pos)
+    for (int r = lo + tid; r < min(hi, m); r += kSelThreads) a.pos_out[bh * a.cap + r] = pos[r];
+  int cnt = 0;
+  if (m < n && m > 0) {
+    const int64_t from = (int64_t)last - a.n_recent;
+    const bool guards = a.n_first + a.n_recent > 0;
+    auto key = [&](int r) {  // of row r, after the first round of counting
+      if (cached) return keys[r - lo + (r - lo) / kRun];
+      if (guards) {
+        const int p = __ldcg(pos + r);
+        if (p < a.n_first || p > from) return kGuarded;
+      }
+      return weight_key(__ldcg(w + r));
+    };
+    // ---- the threshold: keys in [base, base + span] are in question, `need` of them are kept
+    uint32_t base = kmin, span = kmax - kmin;
+    int shift = max(0, 32 - __clz((int)span) - kBinBits);  // span >> shift < kBins
+    int need = m, buf = 0, eq_before = 0;
+    bool ties = false;  // only the first `need` rows of those with key `base` are kept
+    for (bool first = true;; first = false, buf ^= 1) {
+      int* hist = sm.hist[buf];
+      for (int i = tid; i <= kBins; i += kSelThreads) hist[i] = 0;
+      __syncthreads();
+      for (int r0 = lo; r0 < hi; r0 += kSelThreads) {
+        const int r = r0 + tid;
+        int bin = -1;
+        if (r < hi) {
+          uint32_t k;
+          if (first && cached && guards) {
+            const int p = __ldcg(pos + r);
+            uint32_t* kp = &keys[r - lo + (r - lo) / kRun];
+            if (p < a.n_first || p > from) *kp = kGuarded;
+            k = *kp;
+          } else {
+            k = key(r);
+          }
+          const uint32_t d = k - base;
+          if (k == kGuarded)
+            bin = first ? kBins : -1;
+          else if (k >= base && d <= span)
+            bin = (int)(d >> shift);
+        }
+        // rows of equal weight would queue up at one counter
+        int same;
+        __match_all_sync(0xffffffffu, bin, &same);
+        if (same) {
+          if (bin >= 0 && lane == 0) atomicAdd(&hist[bin], 32);
+        } else if (bin >= 0) {
+          atomicAdd(&hist[bin], 1);
+        }
+      }
+      sync();
+      // add up the cluster's counts: thread t has the bins kBins - 1 - 2 t and the one below (largest keys first)
+      int sum[2], guard = 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int bin = kBins - 1 - 2 * tid - i;
+        sum[i] = 0;
+        for (int c = 0; c < C; ++c) sum[i] += (C == 1 ? hist : cl.map_shared_rank(hist, c))[bin];
+      }
+      if (first)
+        for (int c = 0; c < C; ++c) guard += (C == 1 ? hist : cl.map_shared_rank(hist, c))[kBins];
+      if (first && guard >= m) {
+        // the guarded rows alone fill the budget (equal positions): the first of them are kept
+        base = kGuarded;
+        ties = guard > m;
+        need = m;
+        for (int c = 0; c < rank; ++c) eq_before += (C == 1 ? hist : cl.map_shared_rank(hist, c))[kBins];
+        break;
+      }
+      need -= guard;
+      int all;
+      const int above = block_scan(sum[0] + sum[1], all, sm.scan);
+      if (above < need && above + sum[0] + sum[1] >= need) {
+        const bool second = above + sum[0] < need;
+        sm.found = kBins - 1 - 2 * tid - second;
+        sm.found_above = above + (second ? sum[0] : 0);
+        sm.found_count = sum[second];
+      }
+      __syncthreads();
+      const int bin = sm.found, count = sm.found_count;
+      base += (uint32_t)bin << shift;
+      need -= sm.found_above;
+      if (count == need || shift == 0) {
+        ties = count != need;
+        if (ties)
+          for (int c = 0; c < rank; ++c) eq_before += (C == 1 ? hist : cl.map_shared_rank(hist, c))[bin];
+        break;
+      }
+      span = (1u << shift) - 1;
+      shift = max(0, shift - kBinBits);
+      __syncthreads();  // found is read before the next round writes it
+    }
+    // ---- holes and movers, in row order: rounds of kRun consecutive rows per thread
+    const int per_round = kSelThreads * kRun;
+    int32_t* hole = a.hole + bh * a.half;
+    int32_t* move = a.move + bh * a.half;
+    int hole_at = 0, move_at = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+      int eq_at = eq_before, holes = hole_at, movers = move_at;
+      for (int r0 = lo; r0 < hi; r0 += per_round) {
+        const int r = r0 + tid * kRun;
+        uint32_t keep = 0, eq = 0;
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+          if (r + i < hi) {
+            const uint32_t k = key(r + i);
+            if (k > base || (!ties && k == base)) keep |= 1u << i;
+            if (k == base) eq |= 1u << i;
+          }
+        int all;
+        if (ties) {
+          int left = need - eq_at - block_scan(__popc(eq), all, sm.scan);  // places for this thread's equal rows
+          eq_at += all;
+          for (; eq && left > 0; --left) {
+            keep |= eq & (0u - eq);
+            eq &= eq - 1;
+          }
+        }
+        const uint32_t in = r >= hi ? 0u : r + kRun <= hi ? 0xffffu : (1u << (hi - r)) - 1;
+        const uint32_t low = r >= m ? 0u : r + kRun <= m ? 0xffffu : (1u << (m - r)) - 1;
+        uint32_t hm = in & low & ~keep, mm = keep & ~low;
+        const int rk = block_scan(__popc(hm) | __popc(mm) << 16, all, sm.scan);
+        if (pass == 1) {
+          // (k < half unless the weights change under the call where their keys are read again and again)
+          for (int k = holes + (rk & 0xffff); hm && k < a.half; hm &= hm - 1) hole[k++] = r + __ffs(hm) - 1;
+          for (int k = movers + (rk >> 16); mm && k < a.half; mm &= mm - 1) move[k++] = r + __ffs(mm) - 1;
+        }
+        holes += all & 0xffff;
+        movers += all >> 16;
+      }
+      if (pass == 0) {
+        if (tid < C) {
+          SelExchange* to = C == 1 ? &sm.from[0] : cl.map_shared_rank(&sm.from[rank], tid);
+          to->holes = holes;
+          to->movers = movers;
+        }
+        sync();
+        for (int c = 0; c < C; ++c) {
+          if (c < rank) {
+            hole_at += sm.from[c].holes;
+            move_at += sm.from[c].movers;
+          }
+          cnt += sm.from[c].holes;
+        }
+      }
+    }
+  }
+  // (every access to another CTA's shared memory came before the last barrier that its owner passed)
+  if (rank == 0 && tid == 0) {
+    a.count[bh] = min(cnt, (int)a.half);
     a.lens_out[bh] = m;
   }
 }
 
-// Move the listed rows: a warp takes 32 of a pair's moves, a lane looks up one
-// move's rows, then the warp copies the 32 rows' 16-byte words together.
-__global__ void __launch_bounds__(256) kv_move_kernel(EvictArgs a, int ctas_per_pair) {
-  const int64_t bh = blockIdx.x / ctas_per_pair;
-  const int lane = threadIdx.x & 31;
-  const int warp = (blockIdx.x % ctas_per_pair) * 8 + (threadIdx.x >> 5);
-  const int cnt = a.count[bh];
-  const int per_row = 2 * a.words;
-  for (int i0 = warp * 32; i0 < cnt; i0 += ctas_per_pair * 8 * 32) {
+// Move the listed rows, kMoveRows of a pair to a warp: a lane looks up one
+// move, then the warp loads all rows' 16-byte words (K and V) before it stores
+// the first.  The pairs' counts form one list of such units that is cut evenly
+// over the warps of the grid.
+constexpr int kMoveRows = 8;
+constexpr int kMoveThreads = 256;
+
+template <int kWords>
+__global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const __grid_constant__ EvictArgs a) {
+  __shared__ int sh[kMoveThreads / 32], sh_at[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  sm100::grid_dep_wait();
+  // the pair that holds this CTA's first unit, by a block scan over the counts
+  const int per = (a.BH + kMoveThreads - 1) / kMoveThreads;
+  const int b0 = min(a.BH, tid * per), b1 = min(a.BH, b0 + per);
+  int sum = 0;
+  for (int b = b0; b < b1; ++b) sum += (__ldcg(a.count + b) + kMoveRows - 1) / kMoveRows;
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) sh[warp] = inc;
+  __syncthreads();
+  int before = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i < kMoveThreads / 32; ++i) {
+    if (i < warp) before += sh[i];
+    total += sh[i];
+  }
+  const int u0 = (int)((int64_t)total * blockIdx.x / gridDim.x), u1 = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
+  if (u0 == u1) return;
+  int s = before + inc - sum;
+  if (u0 >= s && u0 < s + sum) {
+    int b = b0;
+    for (;; ++b) {
+      const int u = (__ldcg(a.count + b) + kMoveRows - 1) / kMoveRows;
+      if (u0 < s + u) break;
+      s += u;
+    }
+    sh_at[0] = b;
+    sh_at[1] = s;
+  }
+  __syncthreads();
+  int bh = sh_at[0];
+  s = sh_at[1];
+  int cnt = __ldcg(a.count + bh);
+  constexpr int kHalf = kWords / 2;
+  constexpr int kLoads = kMoveRows * kWords / 32;
+  for (int u = u0 + warp; u < u1; u += kMoveThreads / 32) {
+    while (u >= s + (cnt + kMoveRows - 1) / kMoveRows) {
+      s += (cnt + kMoveRows - 1) / kMoveRows;
+      cnt = __ldcg(a.count + ++bh);
+    }
+    const int i0 = (u - s) * kMoveRows, rows = min(kMoveRows, cnt - i0);
     int64_t src = -1, dst = -1;
-    if (i0 + lane < cnt) {
-      const int s = a.move[bh * a.half + i0 + lane], d = a.hole[bh * a.half + i0 + lane];
-      src = a.c.row(bh, s);
-      dst = a.c.row(bh, d);
-      a.w_out[bh * a.cap + d] = a.w[bh * a.cap + s];
-      a.pos_out[bh * a.cap + d] = a.pos[bh * a.cap + s];
+    if (lane < rows) {
+      const int from = __ldcg(a.move + bh * a.half + i0 + lane), to = __ldcg(a.hole + bh * a.half + i0 + lane);
+      src = a.c.row(bh, from);
+      dst = a.c.row(bh, to);
+      a.w_out[bh * a.cap + to] = __ldcg(a.w + bh * a.cap + from);
+      a.pos_out[bh * a.cap + to] = __ldcg(a.pos + bh * a.cap + from);
     }
-    const int n = min(32, cnt - i0);
-    for (int j0 = 0; j0 < n * per_row; j0 += 32) {
-      const int r = (j0 + lane) / per_row, word = (j0 + lane) % per_row;  // r <= 31: per_row is 16, 32 or 64
-      const int64_t s = __shfl_sync(0xffffffffu, src, r), d = __shfl_sync(0xffffffffu, dst, r);
-      const bool is_v = word >= a.words;
-      const int wd = is_v ? word - a.words : word;
-      char* base = is_v ? a.c.v : a.c.k;
-      if (s >= 0 && d >= 0)
-        reinterpret_cast<uint4*>(base + d * a.words * 16)[wd] = reinterpret_cast<const uint4*>(base + s * a.words * 16)[wd];
+    __syncwarp();
+    uint4 v[kLoads];
+    char* d[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int k = (i * 32 + lane) / kWords, word = lane % kWords + (kWords == 64 ? (i & 1) * 32 : 0);
+      const int64_t f = __shfl_sync(0xffffffffu, src, k), t = __shfl_sync(0xffffffffu, dst, k);
+      const bool is_v = word >= kHalf;
+      const int wd = (is_v ? word - kHalf : word) * 16;
+      char* plane = is_v ? a.c.v : a.c.k;
+      d[i] = k < rows && f >= 0 && t >= 0 ? plane + t * (kHalf * 16) + wd : nullptr;
+      if (d[i]) v[i] = __ldcg(reinterpret_cast<const uint4*>(plane + f * (kHalf * 16) + wd));
     }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      if (d[i]) *reinterpret_cast<uint4*>(d[i]) = v[i];
   }
 }
 
@@ -242,10 +480,9 @@ cudaError_t launch_kv_append(const Plan& p, const KvView& c, int n_new, const KV
                              cudaStream_t st) {
   AppendArgs a{};
   a.c = c;
-  a.BH = (int64_t)p.cfg.batch * p.cfg.kv_heads;
   a.H = p.cfg.kv_heads;
   a.n_new = n_new;
-  a.words = p.cfg.d_h * p.esize / 16;
+  a.chunks = (int)ceil_div64(n_new, kAppendRows * kAppendWarps);
   a.K = (const char*)kv.K;
   a.V = (const char*)kv.V;
   a.sb = kv.sb * p.esize;
@@ -257,11 +494,11 @@ cudaError_t launch_kv_append(const Plan& p, const KvView& c, int n_new, const KV
   a.pos = pos;
   a.cap = cap;
   a.tok_w = tok_w;
-  const int rows_blk = 256 / (2 * a.words);
-  const int64_t blocks = a.BH * ceil_div64(n_new, rows_blk);
+  const unsigned grid = (unsigned)(p.cfg.batch * p.cfg.kv_heads) * a.chunks;
+  const int words = p.cfg.d_h * p.esize / 8;
+  auto kern = words == 16 ? kv_append_kernel<16> : words == 32 ? kv_append_kernel<32> : kv_append_kernel<64>;
   ProfScope ps(p, st, KID_KV_APPEND);
-  kv_append_kernel<<<(int)std::min<int64_t>(blocks, kNumSMs * 8), 256, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(kern, grid, kAppendWarps * 32, 0, st, a);
 }
 
 cudaError_t launch_kv_evict(const Plan& p, const KvView& c, const int32_t* budget, int n_first, int n_recent,
@@ -270,7 +507,7 @@ cudaError_t launch_kv_evict(const Plan& p, const KvView& c, const int32_t* budge
   const KvWorkspace L = kv_workspace(p, c.max_len);
   EvictArgs a{};
   a.c = c;
-  a.BH = (int64_t)p.cfg.batch * p.cfg.kv_heads;
+  a.BH = p.cfg.batch * p.cfg.kv_heads;
   a.budget = budget;
   a.n_first = n_first;
   a.n_recent = n_recent;
@@ -284,17 +521,26 @@ cudaError_t launch_kv_evict(const Plan& p, const KvView& c, const int32_t* budge
   a.hole = (int32_t*)((char*)ws + L.hole);
   a.move = (int32_t*)((char*)ws + L.move);
   a.half = c.max_len / 2;
-  a.words = p.cfg.d_h * p.esize / 16;
+  // as many CTAs per pair as keep two on every SM, each with 1024 rows at least
+  a.cluster = 1;
+  while (a.cluster < kMaxCluster && (int64_t)a.BH * a.cluster * 2 <= 2 * kNumSMs && a.cluster * 2 * 1024 <= c.max_len)
+    a.cluster *= 2;
+  const int run = (int)ceil_div64(ceil_div64(c.max_len, a.cluster), kRun) * kRun;
+  const int cached = run <= kSelCached;
+  const size_t smem = cached ? (size_t)(run + run / kRun) * 4 : 0;
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem((const void*)kv_select_kernel, (kSelCached + kSelCached / kRun) * 4, ready, true);
+  if (e != cudaSuccess) return e;
   {
     ProfScope ps(p, st, KID_KV_SELECT);
-    kv_select_kernel<<<(unsigned)a.BH, kSelThreads, 0, st>>>(a);
+    e = launch_pdl_cluster(kv_select_kernel, (unsigned)(a.BH * a.cluster), kSelThreads, a.cluster, smem, st, a, cached);
   }
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int per_pair = (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div64(a.half, 256), kNumSMs * 8 / a.BH));
+  const int words = p.cfg.d_h * p.esize / 8;
+  auto move = words == 16 ? kv_move_kernel<16> : words == 32 ? kv_move_kernel<32> : kv_move_kernel<64>;
+  const int64_t most = a.BH * ceil_div64(a.half, kMoveRows * kMoveThreads / 32);
   ProfScope ps(p, st, KID_KV_MOVE);
-  kv_move_kernel<<<(unsigned)(a.BH * per_pair), 256, 0, st>>>(a, per_pair);
-  return cudaGetLastError();
+  return launch_pdl(move, (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, kNumSMs * 4)), kMoveThreads, 0, st, a);
 }
 
 }  // namespace dkv
