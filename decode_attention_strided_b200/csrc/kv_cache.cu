@@ -12,6 +12,36 @@ namespace dkv {
 
 namespace {
 
+// A warp copies the K and V rows 0 .. rows-1 of a group of kRows to pool rows
+// to(k) (skipped where that is negative): up to eight 16-byte words per lane
+// are loaded before the first is stored.  kWords: words of one row's K and V together (16, 32 or
+// 64); from(k, is_v): a row's address.  Both are called by all lanes alike.
+template <int kWords, int kRows, typename From, typename To>
+__device__ __forceinline__ void copy_rows(int rows, int lane, From from, To to, const KvView& c) {
+  constexpr int kHalf = kWords / 2;
+  constexpr int kLoads = kRows * kWords / 32;
+  constexpr int kPart = kLoads < 8 ? kLoads : 8;  // words in flight per lane: 32 registers
+#pragma unroll
+  for (int i0 = 0; i0 < kLoads; i0 += kPart) {
+    uint4 v[kPart];
+#pragma unroll
+    for (int i = 0; i < kPart; ++i) {
+      const int k = ((i0 + i) * 32 + lane) / kWords, word = lane % kWords + (kWords == 64 ? (i & 1) * 32 : 0);
+      const bool is_v = word >= kHalf;
+      const char* p = from(k, is_v);
+      if (k < rows) v[i] = __ldcg(reinterpret_cast<const uint4*>(p) + (is_v ? word - kHalf : word));
+    }
+#pragma unroll
+    for (int i = 0; i < kPart; ++i) {
+      const int k = ((i0 + i) * 32 + lane) / kWords, word = lane % kWords + (kWords == 64 ? (i & 1) * 32 : 0);
+      const bool is_v = word >= kHalf;
+      const int64_t t = to(k);
+      if (k < rows && t >= 0)
+        reinterpret_cast<uint4*>((is_v ? c.v : c.k) + t * (kHalf * 16))[is_v ? word - kHalf : word] = v[i];
+    }
+  }
+}
+
 // ---- append
 // A warp copies kAppendRows new rows of a pair: a lane looks up where one row
 // goes, then the warp loads all rows' 16-byte words (K and V) before it stores
@@ -35,7 +65,7 @@ struct AppendArgs {
 
 // kWords: 16-byte words of one row's K and V together (16, 32 or 64).
 template <int kWords>
-__global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kAppendWarps * 32, 4) kv_append_kernel(const __grid_constant__ AppendArgs a) {
   const int bh = blockIdx.x / a.chunks;
   const int b = bh / a.H, h = bh - b * a.H;
   const int lane = threadIdx.x & 31;
@@ -57,23 +87,10 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(const __gr
     if (a.pos) a.pos[bh * a.cap + r] = a.first_pos[b] + t;
   }
   __syncwarp();
-  constexpr int kHalf = kWords / 2;
-  constexpr int kLoads = kAppendRows * kWords / 32;
   const int64_t src = b * a.sb + h * a.sh + (int64_t)t0 * a.st;
-  uint4 v[kLoads];
-  char* dst[kLoads];
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int k = (i * 32 + lane) / kWords, word = lane % kWords + (kWords == 64 ? (i & 1) * 32 : 0);
-    const int64_t to = __shfl_sync(0xffffffffu, row, k);
-    const bool is_v = word >= kHalf;
-    const int wd = is_v ? word - kHalf : word;
-    dst[i] = k < rows && to >= 0 ? (is_v ? a.c.v : a.c.k) + to * (kHalf * 16) + wd * 16 : nullptr;
-    if (dst[i]) v[i] = __ldcg(reinterpret_cast<const uint4*>((is_v ? a.V : a.K) + src + k * a.st) + wd);
-  }
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i)
-    if (dst[i]) *reinterpret_cast<uint4*>(dst[i]) = v[i];
+  copy_rows<kWords, kAppendRows>(
+      rows, lane, [&](int k, bool is_v) { return (is_v ? a.V : a.K) + src + k * a.st; },
+      [&](int k) { return __shfl_sync(0xffffffffu, row, k); }, a.c);
 }
 
 // ---- evict
@@ -94,6 +111,7 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBinBits = 10;
 constexpr int kBins = 1 << kBinBits;
 constexpr int kRun = 16;              // consecutive rows per thread in the scan
+constexpr int kBatch = 4;             // rows per thread in flight
 constexpr int kSelCached = 24 * 1024; // rows per CTA whose keys shared memory holds (two CTAs per SM)
 constexpr int kMaxCluster = 16;
 
@@ -155,7 +173,7 @@ struct SelExchange {
 };
 
 struct SelSmem {
-  int hist[2][kBins + 1];        // the last bin: guarded rows
+  alignas(8) int hist[2][kBins + 2];  // bin kBins: guarded rows
   SelExchange from[kMaxCluster]; // written by the CTAs of the cluster
   int scan[32];
   uint32_t rmin[kSelWarps], rmax[kSelWarps];
@@ -190,13 +208,24 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
   // ---- keys of this CTA's rows, their range, the largest position, and the pages
   uint32_t kmin = 0xffffffffu, kmax = 0u;
   int last = INT32_MIN, bad = 0;
-#pragma unroll 4
-  for (int r = lo + tid; r < hi; r += kSelThreads) {
-    const uint32_t k = weight_key(__ldcg(w + r));
-    if (cached) keys[r - lo + (r - lo) / kRun] = k;
-    kmin = min(kmin, k);
-    kmax = max(kmax, k);
-    last = max(last, __ldcg(pos + r));
+  for (int r0 = lo + tid; r0 < hi; r0 += kBatch * kSelThreads) {
+    float wv[kBatch];
+    int pv[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = min(r0 + i * kSelThreads, hi - 1);  // (a row twice does no harm)
+      wv[i] = __ldcg(w + r);
+      pv[i] = __ldcg(pos + r);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = min(r0 + i * kSelThreads, hi - 1);
+      const uint32_t k = weight_key(wv[i]);
+      if (cached) keys[r - lo + (r - lo) / kRun] = k;
+      kmin = min(kmin, k);
+      kmax = max(kmax, k);
+      last = max(last, pv[i]);
+    }
   }
   // the pages of the rows this CTA starts with
   for (int r = ((lo >> a.c.page_log) + tid) << a.c.page_log; r < hi; r += kSelThreads << a.c.page_log)
@@ -233,10 +262,24 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
   }
   if (bad || budget < 0) m = n;
   // rows below m start out as themselves; the move writes over the holes
-  if (a.w_out != a.w)
-    for (int r = lo + tid; r < min(hi, m); r += kSelThreads) a.w_out[bh * a.cap + r] = w[r];
-  if (a.pos_out != a.pos)
-    for (int r = lo + tid; r < min(hi, m); r += kSelThreads) a.pos_out[bh * a.cap + r] = pos[r];
+  if (a.w_out != a.w || a.pos_out != a.pos) {
+    for (int r0 = rank * kSelThreads + tid; r0 < m; r0 += kBatch * C * kSelThreads) {
+      float wv[kBatch];
+      int pv[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = min(r0 + i * C * kSelThreads, m - 1);
+        wv[i] = __ldcg(w + r);
+        pv[i] = __ldcg(pos + r);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = r0 + i * C * kSelThreads;
+        if (r < m && a.w_out != a.w) a.w_out[bh * a.cap + r] = wv[i];
+        if (r < m && a.pos_out != a.pos) a.pos_out[bh * a.cap + r] = pv[i];
+      }
+    }
+  }
   int cnt = 0;
   if (m < n && m > 0) {
     const int64_t from = (int64_t)last - a.n_recent;
@@ -258,45 +301,63 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
       int* hist = sm.hist[buf];
       for (int i = tid; i <= kBins; i += kSelThreads) hist[i] = 0;
       __syncthreads();
-      for (int r0 = lo; r0 < hi; r0 += kSelThreads) {
-        const int r = r0 + tid;
-        int bin = -1;
-        if (r < hi) {
-          uint32_t k;
-          if (first && cached && guards) {
-            const int p = __ldcg(pos + r);
+      for (int r0 = lo; r0 < hi; r0 += kBatch * kSelThreads) {
+        uint32_t kv[kBatch];
+        if (first && cached && guards) {
+          int pv[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) pv[i] = __ldcg(pos + min(r0 + i * kSelThreads + tid, hi - 1));
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int r = min(r0 + i * kSelThreads + tid, hi - 1);
             uint32_t* kp = &keys[r - lo + (r - lo) / kRun];
-            if (p < a.n_first || p > from) *kp = kGuarded;
-            k = *kp;
-          } else {
-            k = key(r);
+            if (pv[i] < a.n_first || pv[i] > from) *kp = kGuarded;
+            kv[i] = *kp;
           }
-          const uint32_t d = k - base;
-          if (k == kGuarded)
-            bin = first ? kBins : -1;
-          else if (k >= base && d <= span)
-            bin = (int)(d >> shift);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) kv[i] = key(min(r0 + i * kSelThreads + tid, hi - 1));
         }
-        // rows of equal weight would queue up at one counter
-        int same;
-        __match_all_sync(0xffffffffu, bin, &same);
-        if (same) {
-          if (bin >= 0 && lane == 0) atomicAdd(&hist[bin], 32);
-        } else if (bin >= 0) {
-          atomicAdd(&hist[bin], 1);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          if (r0 + i * kSelThreads >= hi) break;
+          const uint32_t k = kv[i], d = k - base;
+          int bin = -1;
+          if (r0 + i * kSelThreads + tid < hi) {
+            if (k == kGuarded)
+              bin = first ? kBins : -1;
+            else if (k >= base && d <= span)
+              bin = (int)(d >> shift);
+          }
+          // rows of equal weight would queue up at one counter
+          int same;
+          __match_all_sync(0xffffffffu, bin, &same);
+          if (same) {
+            if (bin >= 0 && lane == 0) atomicAdd(&hist[bin], 32);
+          } else if (bin >= 0) {
+            atomicAdd(&hist[bin], 1);
+          }
         }
       }
       sync();
       // add up the cluster's counts: thread t has the bins kBins - 1 - 2 t and the one below (largest keys first)
-      int sum[2], guard = 0;
+      int sum[2] = {0, 0}, guard = 0;
+      {
+        const int at = kBins - 2 - 2 * tid;
+        int2 got[kMaxCluster];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int bin = kBins - 1 - 2 * tid - i;
-        sum[i] = 0;
-        for (int c = 0; c < C; ++c) sum[i] += (C == 1 ? hist : cl.map_shared_rank(hist, c))[bin];
+        for (int c = 0; c < kMaxCluster; ++c)
+          if (c < C) got[c] = *reinterpret_cast<const int2*>((C == 1 ? hist : cl.map_shared_rank(hist, c)) + at);
+        int gv = 0;
+        if (first && lane < C) gv = (C == 1 ? hist : cl.map_shared_rank(hist, lane))[kBins];
+        guard = __reduce_add_sync(0xffffffffu, gv);
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c)
+          if (c < C) {
+            sum[0] += got[c].y;
+            sum[1] += got[c].x;
+          }
       }
-      if (first)
-        for (int c = 0; c < C; ++c) guard += (C == 1 ? hist : cl.map_shared_rank(hist, c))[kBins];
       if (first && guard >= m) {
         // the guarded rows alone fill the budget (equal positions): the first of them are kept
         base = kGuarded;
@@ -333,31 +394,36 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
     int32_t* hole = a.hole + bh * a.half;
     int32_t* move = a.move + bh * a.half;
     int hole_at = 0, move_at = 0;
+    uint32_t hm = 0, mm = 0;  // holes and movers of this thread's run in the last round counted
+    int rk = 0;
     for (int pass = 0; pass < 2; ++pass) {
       int eq_at = eq_before, holes = hole_at, movers = move_at;
       for (int r0 = lo; r0 < hi; r0 += per_round) {
         const int r = r0 + tid * kRun;
-        uint32_t keep = 0, eq = 0;
+        int all = 0;
+        if (pass == 0 || run > per_round) {  // one round: the first pass has it all
+          uint32_t keep = 0, eq = 0;
 #pragma unroll
-        for (int i = 0; i < kRun; ++i)
-          if (r + i < hi) {
-            const uint32_t k = key(r + i);
-            if (k > base || (!ties && k == base)) keep |= 1u << i;
-            if (k == base) eq |= 1u << i;
+          for (int i = 0; i < kRun; ++i)
+            if (r + i < hi) {
+              const uint32_t k = key(r + i);
+              if (k > base || (!ties && k == base)) keep |= 1u << i;
+              if (k == base) eq |= 1u << i;
+            }
+          if (ties) {
+            int left = need - eq_at - block_scan(__popc(eq), all, sm.scan);  // places for this thread's equal rows
+            eq_at += all;
+            for (; eq && left > 0; --left) {
+              keep |= eq & (0u - eq);
+              eq &= eq - 1;
+            }
           }
-        int all;
-        if (ties) {
-          int left = need - eq_at - block_scan(__popc(eq), all, sm.scan);  // places for this thread's equal rows
-          eq_at += all;
-          for (; eq && left > 0; --left) {
-            keep |= eq & (0u - eq);
-            eq &= eq - 1;
-          }
+          const uint32_t in = r >= hi ? 0u : r + kRun <= hi ? 0xffffu : (1u << (hi - r)) - 1;
+          const uint32_t low = r >= m ? 0u : r + kRun <= m ? 0xffffu : (1u << (m - r)) - 1;
+          hm = in & low & ~keep;
+          mm = keep & ~low;
+          rk = block_scan(__popc(hm) | __popc(mm) << 16, all, sm.scan);
         }
-        const uint32_t in = r >= hi ? 0u : r + kRun <= hi ? 0xffffu : (1u << (hi - r)) - 1;
-        const uint32_t low = r >= m ? 0u : r + kRun <= m ? 0xffffu : (1u << (m - r)) - 1;
-        uint32_t hm = in & low & ~keep, mm = keep & ~low;
-        const int rk = block_scan(__popc(hm) | __popc(mm) << 16, all, sm.scan);
         if (pass == 1) {
           // (k < half unless the weights change under the call where their keys are read again and again)
           for (int k = holes + (rk & 0xffff); hm && k < a.half; hm &= hm - 1) hole[k++] = r + __ffs(hm) - 1;
@@ -398,7 +464,7 @@ constexpr int kMoveRows = 8;
 constexpr int kMoveThreads = 256;
 
 template <int kWords>
-__global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, 4) kv_move_kernel(const __grid_constant__ EvictArgs a) {
   __shared__ int sh[kMoveThreads / 32], sh_at[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   sm100::grid_dep_wait();
@@ -438,8 +504,6 @@ __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const __grid_cons
   int bh = sh_at[0];
   s = sh_at[1];
   int cnt = __ldcg(a.count + bh);
-  constexpr int kHalf = kWords / 2;
-  constexpr int kLoads = kMoveRows * kWords / 32;
   for (int u = u0 + warp; u < u1; u += kMoveThreads / 32) {
     while (u >= s + (cnt + kMoveRows - 1) / kMoveRows) {
       s += (cnt + kMoveRows - 1) / kMoveRows;
@@ -454,22 +518,13 @@ __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const __grid_cons
       a.w_out[bh * a.cap + to] = __ldcg(a.w + bh * a.cap + from);
       a.pos_out[bh * a.cap + to] = __ldcg(a.pos + bh * a.cap + from);
     }
+    // a row without a place is neither read nor written
+    if (src < 0 || dst < 0) src = 0, dst = -1;
     __syncwarp();
-    uint4 v[kLoads];
-    char* d[kLoads];
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int k = (i * 32 + lane) / kWords, word = lane % kWords + (kWords == 64 ? (i & 1) * 32 : 0);
-      const int64_t f = __shfl_sync(0xffffffffu, src, k), t = __shfl_sync(0xffffffffu, dst, k);
-      const bool is_v = word >= kHalf;
-      const int wd = (is_v ? word - kHalf : word) * 16;
-      char* plane = is_v ? a.c.v : a.c.k;
-      d[i] = k < rows && f >= 0 && t >= 0 ? plane + t * (kHalf * 16) + wd : nullptr;
-      if (d[i]) v[i] = __ldcg(reinterpret_cast<const uint4*>(plane + f * (kHalf * 16) + wd));
-    }
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-      if (d[i]) *reinterpret_cast<uint4*>(d[i]) = v[i];
+    copy_rows<kWords, kMoveRows>(
+        rows, lane,
+        [&](int k, bool is_v) { return (is_v ? a.c.v : a.c.k) + __shfl_sync(0xffffffffu, src, k) * (kWords * 8); },
+        [&](int k) { return __shfl_sync(0xffffffffu, dst, k); }, a.c);
   }
 }
 
