@@ -50,10 +50,9 @@ cudaError_t launch_pdl_cluster(void (*kern)(P...), unsigned grid, unsigned threa
   return cudaLaunchKernelEx(&cfg, kern, P(args)...);
 }
 
-// Let a kernel use `smem` bytes of dynamic shared memory (and clusters of more
-// than eight CTAs) on the current device; `ready` keeps the devices, of the
-// first 64, that have it already.
-inline cudaError_t allow_smem(const void* kern, size_t smem, std::atomic<uint64_t>& ready, bool large_cluster = false) {
+// Let a kernel use `smem` bytes of dynamic shared memory on the current device;
+// `ready` keeps the devices, of the first 64, that have it already.
+inline cudaError_t allow_smem(const void* kern, size_t smem, std::atomic<uint64_t>& ready) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -62,8 +61,6 @@ inline cudaError_t allow_smem(const void* kern, size_t smem, std::atomic<uint64_
   if (smem) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   // the whole L1 as shared memory for all kernels of a call: an SM need not be reconfigured between them
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-  if (e == cudaSuccess && large_cluster)
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }

@@ -100,20 +100,24 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) kv_append_kernel(const _
 // bins over it, counted per CTA and added up over the cluster through
 // distributed shared memory, until the bin that holds the m-th key is kept
 // whole or holds one key only; two rounds as a rule, three or four at most.
+// (A cache held at its budget drops a row or so per token: up to kFew rows are
+// found as that many minima instead, and moved at once.)
 // Rows above the threshold and the first of those equal to it are kept; a scan
 // in row order numbers the dropped rows below m (holes) and the kept rows at or
 // past m (movers), of which there are equally many: mover i goes to hole i.
 // Bound by its chain of block and cluster barriers: the keys are read once.  A
 // second kernel moves the rows, spread over the whole GPU whatever the pairs'
 // shares: bound by the rows read and written.
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBinBits = 10;
 constexpr int kBins = 1 << kBinBits;
 constexpr int kRun = 16;              // consecutive rows per thread in the scan
 constexpr int kBatch = 4;             // rows per thread in flight
-constexpr int kSelCached = 24 * 1024; // rows per CTA whose keys shared memory holds (two CTAs per SM)
-constexpr int kMaxCluster = 16;
+constexpr int kSelCached = 48 * 1024; // rows per CTA whose keys shared memory holds
+constexpr int kMaxCluster = 8;
+constexpr int kFew = 4;               // this many rows to drop are found one by one
+static_assert(kBins == kSelThreads && kSelWarps == 32, "a thread per bin, a lane per warp");
 
 struct EvictArgs {
   KvView c;
@@ -130,6 +134,7 @@ struct EvictArgs {
   int32_t* hole;   // [BH][half]
   int32_t* move;   // [BH][half]
   int64_t half;
+  int words;       // 16-byte words of one K row
 };
 
 constexpr uint32_t kGuarded = 0xffffffffu;  // above every weight's key
@@ -154,7 +159,7 @@ __device__ __forceinline__ int block_scan(int v, int& all, int* sh) {
   __syncthreads();
   if (lane == 31) sh[warp] = inc;
   __syncthreads();
-  const int t = lane < kSelWarps ? sh[lane] : 0;
+  const int t = sh[lane];
   int ti = t;
 #pragma unroll
   for (int o = 1; o < kSelWarps; o <<= 1) {
@@ -170,14 +175,16 @@ struct SelExchange {
   uint32_t kmin, kmax;
   int last, bad;      // largest position; a page out of range
   int holes, movers;
+  uint64_t least[kFew];
 };
 
 struct SelSmem {
-  alignas(8) int hist[2][kBins + 2];  // bin kBins: guarded rows
+  int hist[2][kBins + 1];  // bin kBins: guarded rows
   SelExchange from[kMaxCluster]; // written by the CTAs of the cluster
   int scan[32];
   uint32_t rmin[kSelWarps], rmax[kSelWarps];
   int rlast[kSelWarps];
+  uint64_t rleast[kSelWarps];
   int found, found_count, found_above;
 };
 
@@ -208,17 +215,17 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
   // ---- keys of this CTA's rows, their range, the largest position, and the pages
   uint32_t kmin = 0xffffffffu, kmax = 0u;
   int last = INT32_MIN, bad = 0;
-  for (int r0 = lo + tid; r0 < hi; r0 += kBatch * kSelThreads) {
-    float wv[kBatch];
-    int pv[kBatch];
+  for (int r0 = lo + tid; r0 < hi; r0 += 2 * kBatch * kSelThreads) {
+    float wv[2 * kBatch];
+    int pv[2 * kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < 2 * kBatch; ++i) {
       const int r = min(r0 + i * kSelThreads, hi - 1);  // (a row twice does no harm)
       wv[i] = __ldcg(w + r);
       pv[i] = __ldcg(pos + r);
     }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < 2 * kBatch; ++i) {
       const int r = min(r0 + i * kSelThreads, hi - 1);
       const uint32_t k = weight_key(wv[i]);
       if (cached) keys[r - lo + (r - lo) / kRun] = k;
@@ -241,10 +248,9 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
   bad = __syncthreads_or(bad);
   if (C > 1) cg::cluster_group::barrier_wait();
   if (warp == 0) {
-    const int s = lane % kSelWarps;
-    kmin = __reduce_min_sync(0xffffffffu, sm.rmin[s]);
-    kmax = __reduce_max_sync(0xffffffffu, sm.rmax[s]);
-    last = __reduce_max_sync(0xffffffffu, sm.rlast[s]);
+    kmin = __reduce_min_sync(0xffffffffu, sm.rmin[lane]);
+    kmax = __reduce_max_sync(0xffffffffu, sm.rmax[lane]);
+    last = __reduce_max_sync(0xffffffffu, sm.rlast[lane]);
     if (lane < C) {
       SelExchange* to = C == 1 ? &sm.from[0] : cl.map_shared_rank(&sm.from[rank], lane);
       to->kmin = kmin;
@@ -281,17 +287,93 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
     }
   }
   int cnt = 0;
-  if (m < n && m > 0) {
-    const int64_t from = (int64_t)last - a.n_recent;
-    const bool guards = a.n_first + a.n_recent > 0;
-    auto key = [&](int r) {  // of row r, after the first round of counting
-      if (cached) return keys[r - lo + (r - lo) / kRun];
-      if (guards) {
-        const int p = __ldcg(pos + r);
-        if (p < a.n_first || p > from) return kGuarded;
+  const int64_t from = (int64_t)last - a.n_recent;
+  const bool guards = a.n_first + a.n_recent > 0;
+  // key of row r; `guard`: before the cached keys of guarded rows are marked
+  auto key = [&](int r, bool guard) {
+    uint32_t* kp = cached ? &keys[r - lo + (r - lo) / kRun] : nullptr;
+    uint32_t k = cached ? *kp : weight_key(__ldcg(w + r));
+    if (guards && (guard || !cached)) {
+      const int p = __ldcg(pos + r);
+      if (p < a.n_first || p > from) {
+        k = kGuarded;
+        if (cached) *kp = k;
       }
-      return weight_key(__ldcg(w + r));
-    };
+    }
+    return k;
+  };
+  if (m < n && m > 0 && n - m <= kFew) {
+    // ---- the n - m least rows, the higher of equal ones first
+    int drop[kFew];
+#pragma unroll
+    for (int i = 0; i < kFew; ++i) {
+      if (i >= n - m) break;
+      uint64_t least = ~0ull;
+      for (int r0 = lo; r0 < hi; r0 += kBatch * kSelThreads) {
+        uint32_t kv[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) kv[j] = key(min(r0 + j * kSelThreads + tid, hi - 1), i == 0);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int r = min(r0 + j * kSelThreads + tid, hi - 1);
+          uint64_t v = (uint64_t)kv[j] << 32 | (uint32_t)~r;
+#pragma unroll
+          for (int d = 0; d < i; ++d)
+            if (drop[d] == r) v = ~0ull;
+          least = min(least, v);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+      __syncthreads();  // (the last turn's rleast has been read)
+      if (lane == 0) sm.rleast[warp] = least;
+      __syncthreads();
+      if (warp == 0) {
+        least = sm.rleast[lane];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+        if (lane < C) (C == 1 ? &sm.from[0] : cl.map_shared_rank(&sm.from[rank], lane))->least[i] = least;
+      }
+      sync();
+      least = sm.from[0].least[i];
+      for (int c = 1; c < C; ++c) least = min(least, sm.from[c].least[i]);
+      drop[i] = (int)~(uint32_t)least;
+    }
+    // the k-th kept row at or past m goes to the k-th dropped row below m
+    if (rank == 0 && warp < n - m) {
+      auto dropped = [&](int r) {
+        bool is = false;
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) is |= i < n - m && drop[i] == r;
+        return is;
+      };
+      int src = -1, dst = -1;
+      for (int r = m, k = 0; r < n; ++r)
+        if (!dropped(r) && k++ == warp) src = r;
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) {
+        if (i >= n - m || drop[i] >= m) continue;
+        int below = 0;
+#pragma unroll
+        for (int d = 0; d < kFew; ++d) below += d < n - m && drop[d] < drop[i];
+        if (below == warp) dst = drop[i];
+      }
+      if (src >= 0 && dst >= 0) {
+        const int64_t ps = a.c.row(bh, src), pd = a.c.row(bh, dst);
+        if (ps >= 0 && pd >= 0)
+          for (int i = lane; i < 2 * a.words; i += 32) {
+            char* plane = i >= a.words ? a.c.v : a.c.k;
+            const int wd = i >= a.words ? i - a.words : i;
+            reinterpret_cast<uint4*>(plane + pd * a.words * 16)[wd] =
+                __ldcg(reinterpret_cast<const uint4*>(plane + ps * a.words * 16) + wd);
+          }
+        if (lane == 0) {
+          a.w_out[bh * a.cap + dst] = __ldcg(w + src);
+          a.pos_out[bh * a.cap + dst] = __ldcg(pos + src);
+        }
+      }
+    }
+  } else if (m < n && m > 0) {
     // ---- the threshold: keys in [base, base + span] are in question, `need` of them are kept
     uint32_t base = kmin, span = kmax - kmin;
     int shift = max(0, 32 - __clz((int)span) - kBinBits);  // span >> shift < kBins
@@ -303,21 +385,8 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
       __syncthreads();
       for (int r0 = lo; r0 < hi; r0 += kBatch * kSelThreads) {
         uint32_t kv[kBatch];
-        if (first && cached && guards) {
-          int pv[kBatch];
 #pragma unroll
-          for (int i = 0; i < kBatch; ++i) pv[i] = __ldcg(pos + min(r0 + i * kSelThreads + tid, hi - 1));
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int r = min(r0 + i * kSelThreads + tid, hi - 1);
-            uint32_t* kp = &keys[r - lo + (r - lo) / kRun];
-            if (pv[i] < a.n_first || pv[i] > from) *kp = kGuarded;
-            kv[i] = *kp;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) kv[i] = key(min(r0 + i * kSelThreads + tid, hi - 1));
-        }
+        for (int i = 0; i < kBatch; ++i) kv[i] = key(min(r0 + i * kSelThreads + tid, hi - 1), first);
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
           if (r0 + i * kSelThreads >= hi) break;
@@ -329,34 +398,28 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
             else if (k >= base && d <= span)
               bin = (int)(d >> shift);
           }
+          if (!__any_sync(0xffffffffu, bin >= 0)) continue;
           // rows of equal weight would queue up at one counter
-          int same;
-          __match_all_sync(0xffffffffu, bin, &same);
-          if (same) {
-            if (bin >= 0 && lane == 0) atomicAdd(&hist[bin], 32);
+          if (__all_sync(0xffffffffu, bin == __shfl_sync(0xffffffffu, bin, 0))) {
+            if (lane == 0) atomicAdd(&hist[bin], 32);
           } else if (bin >= 0) {
             atomicAdd(&hist[bin], 1);
           }
         }
       }
       sync();
-      // add up the cluster's counts: thread t has the bins kBins - 1 - 2 t and the one below (largest keys first)
-      int sum[2] = {0, 0}, guard = 0;
+      // add up the cluster's counts: thread t has bin kBins - 1 - t (largest keys first)
+      int sum = 0, guard = 0;
       {
-        const int at = kBins - 2 - 2 * tid;
-        int2 got[kMaxCluster];
+        int got[kMaxCluster];
 #pragma unroll
         for (int c = 0; c < kMaxCluster; ++c)
-          if (c < C) got[c] = *reinterpret_cast<const int2*>((C == 1 ? hist : cl.map_shared_rank(hist, c)) + at);
+          got[c] = c < C ? (C == 1 ? hist : cl.map_shared_rank(hist, c))[kBins - 1 - tid] : 0;
         int gv = 0;
         if (first && lane < C) gv = (C == 1 ? hist : cl.map_shared_rank(hist, lane))[kBins];
         guard = __reduce_add_sync(0xffffffffu, gv);
 #pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c)
-          if (c < C) {
-            sum[0] += got[c].y;
-            sum[1] += got[c].x;
-          }
+        for (int c = 0; c < kMaxCluster; ++c) sum += got[c];
       }
       if (first && guard >= m) {
         // the guarded rows alone fill the budget (equal positions): the first of them are kept
@@ -368,12 +431,11 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
       }
       need -= guard;
       int all;
-      const int above = block_scan(sum[0] + sum[1], all, sm.scan);
-      if (above < need && above + sum[0] + sum[1] >= need) {
-        const bool second = above + sum[0] < need;
-        sm.found = kBins - 1 - 2 * tid - second;
-        sm.found_above = above + (second ? sum[0] : 0);
-        sm.found_count = sum[second];
+      const int above = block_scan(sum, all, sm.scan);
+      if (above < need && above + sum >= need) {
+        sm.found = kBins - 1 - tid;
+        sm.found_above = above;
+        sm.found_count = sum;
       }
       __syncthreads();
       const int bin = sm.found, count = sm.found_count;
@@ -406,7 +468,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
 #pragma unroll
           for (int i = 0; i < kRun; ++i)
             if (r + i < hi) {
-              const uint32_t k = key(r + i);
+              const uint32_t k = key(r + i, false);
               if (k > base || (!ties && k == base)) keep |= 1u << i;
               if (k == base) eq |= 1u << i;
             }
@@ -576,15 +638,16 @@ cudaError_t launch_kv_evict(const Plan& p, const KvView& c, const int32_t* budge
   a.hole = (int32_t*)((char*)ws + L.hole);
   a.move = (int32_t*)((char*)ws + L.move);
   a.half = c.max_len / 2;
-  // as many CTAs per pair as keep two on every SM, each with 1024 rows at least
+  a.words = p.cfg.d_h * p.esize / 16;
+  // as many CTAs per pair as the SMs hold at once (one each), each with 1024 rows at least
   a.cluster = 1;
-  while (a.cluster < kMaxCluster && (int64_t)a.BH * a.cluster * 2 <= 2 * kNumSMs && a.cluster * 2 * 1024 <= c.max_len)
+  while (a.cluster < kMaxCluster && (int64_t)a.BH * a.cluster * 2 <= kNumSMs && a.cluster * 2 * 1024 <= c.max_len)
     a.cluster *= 2;
   const int run = (int)ceil_div64(ceil_div64(c.max_len, a.cluster), kRun) * kRun;
   const int cached = run <= kSelCached;
   const size_t smem = cached ? (size_t)(run + run / kRun) * 4 : 0;
   static std::atomic<uint64_t> ready{0};
-  cudaError_t e = allow_smem((const void*)kv_select_kernel, (kSelCached + kSelCached / kRun) * 4, ready, true);
+  cudaError_t e = allow_smem((const void*)kv_select_kernel, (kSelCached + kSelCached / kRun) * 4, ready);
   if (e != cudaSuccess) return e;
   {
     ProfScope ps(p, st, KID_KV_SELECT);
