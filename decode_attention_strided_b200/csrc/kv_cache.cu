@@ -105,16 +105,17 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) kv_append_kernel(const _
 // Rows above the threshold and the first of those equal to it are kept; a scan
 // in row order numbers the dropped rows below m (holes) and the kept rows at or
 // past m (movers), of which there are equally many: mover i goes to hole i.
-// Bound by its chain of block and cluster barriers: the keys are read once.  A
-// second kernel moves the rows, spread over the whole GPU whatever the pairs'
-// shares: bound by the rows read and written.
+// Bound by its chain of block and cluster barriers: the keys are read once.
+// Where the moves are few for certain, the clusters make them; else a second
+// kernel does, spread over the whole GPU whatever the pairs' shares: bound by
+// the rows read and written.
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBinBits = 10;
 constexpr int kBins = 1 << kBinBits;
-constexpr int kRun = 16;              // consecutive rows per thread in the scan
+constexpr int kRun = 512;             // consecutive rows per warp in the scan
 constexpr int kBatch = 4;             // rows per thread in flight
-constexpr int kSelCached = 48 * 1024; // rows per CTA whose keys shared memory holds
+constexpr int kSelCached = 24 * 1024; // rows per CTA whose keys and positions shared memory holds
 constexpr int kMaxCluster = 8;
 constexpr int kFew = 4;               // this many rows to drop are found one by one
 static_assert(kBins == kSelThreads && kSelWarps == 32, "a thread per bin, a lane per warp");
@@ -134,7 +135,6 @@ struct EvictArgs {
   int32_t* hole;   // [BH][half]
   int32_t* move;   // [BH][half]
   int64_t half;
-  int words;       // 16-byte words of one K row
 };
 
 constexpr uint32_t kGuarded = 0xffffffffu;  // above every weight's key
@@ -170,6 +170,17 @@ __device__ __forceinline__ int block_scan(int v, int& all, int* sh) {
   return __shfl_sync(0xffffffffu, ti - t, warp) + inc - v;
 }
 
+// The same for a value that is the warp's, not the thread's.
+__device__ __forceinline__ int warps_scan(int v, int& all, int* sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncthreads();
+  if (lane == 0) sh[warp] = v;
+  __syncthreads();
+  const int t = sh[lane];
+  all = __reduce_add_sync(0xffffffffu, t);
+  return __reduce_add_sync(0xffffffffu, lane < warp ? t : 0);
+}
+
 // What a CTA tells the others of its cluster.
 struct SelExchange {
   uint32_t kmin, kmax;
@@ -188,9 +199,32 @@ struct SelSmem {
   int found, found_count, found_above;
 };
 
-__global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_constant__ EvictArgs a, int cached) {
+// Moves i0 .. i0 + rows - 1 of a pair (rows <= kRows), by one warp: a lane
+// looks up one move, then the warp copies the rows.
+template <int kWords, int kRows>
+__device__ __forceinline__ void move_rows(const EvictArgs& a, int bh, int i0, int rows, int lane) {
+  int64_t src = 0, dst = -1;
+  if (lane < rows) {
+    const int from = __ldcg(a.move + bh * a.half + i0 + lane), to = __ldcg(a.hole + bh * a.half + i0 + lane);
+    const int64_t s = a.c.row(bh, from), d = a.c.row(bh, to);
+    if (s >= 0 && d >= 0) src = s, dst = d;  // (a row without a place is neither read nor written)
+    a.w_out[bh * a.cap + to] = __ldcg(a.w + bh * a.cap + from);
+    a.pos_out[bh * a.cap + to] = __ldcg(a.pos + bh * a.cap + from);
+  }
+  __syncwarp();
+  copy_rows<kWords, kRows>(
+      rows, lane,
+      [&](int k, bool is_v) { return (is_v ? a.c.v : a.c.k) + __shfl_sync(0xffffffffu, src, k) * (kWords * 8); },
+      [&](int k) { return __shfl_sync(0xffffffffu, dst, k); }, a.c);
+}
+
+// cached: the rows' keys and positions fit shared memory; all_here: the
+// clusters make all moves, not the few of a step alone.
+template <int kWords>
+__global__ void __launch_bounds__(kSelThreads)
+    kv_select_kernel(const __grid_constant__ EvictArgs a, int cached, int all_here) {
   namespace cg = cooperative_groups;
-  extern __shared__ uint32_t keys[];  // row lo + i at i + i / kRun: a thread's run meets all banks
+  extern __shared__ uint32_t keys[];  // [run], then the positions
   __shared__ SelSmem sm;
   const cg::cluster_group cl = cg::this_cluster();
   const int C = a.cluster, rank = C == 1 ? 0 : (int)cl.block_rank();
@@ -204,7 +238,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
   if (rank == 0 && tid == 0 && (raw != n || budget < 0)) a.c.report((uint32_t)(raw != n ? raw : budget));
   const float* w = a.w + bh * a.cap;
   const int32_t* pos = a.pos + bh * a.cap;
-  const int run = ((n + C - 1) / C + kRun - 1) / kRun * kRun;  // rows per CTA
+  const int run = (n + C - 1) / C;  // rows per CTA
   const int lo = min(n, rank * run), hi = min(n, lo + run);
   auto sync = [&] {
     if (C == 1)
@@ -215,20 +249,25 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
   // ---- keys of this CTA's rows, their range, the largest position, and the pages
   uint32_t kmin = 0xffffffffu, kmax = 0u;
   int last = INT32_MIN, bad = 0;
+  int* spos = reinterpret_cast<int*>(keys) + run;
   for (int r0 = lo + tid; r0 < hi; r0 += 2 * kBatch * kSelThreads) {
     float wv[2 * kBatch];
     int pv[2 * kBatch];
 #pragma unroll
     for (int i = 0; i < 2 * kBatch; ++i) {
-      const int r = min(r0 + i * kSelThreads, hi - 1);  // (a row twice does no harm)
-      wv[i] = __ldcg(w + r);
-      pv[i] = __ldcg(pos + r);
+      const int r = r0 + i * kSelThreads;
+      wv[i] = r < hi ? __ldcg(w + r) : 0.f;
+      pv[i] = r < hi ? __ldcg(pos + r) : 0;
     }
 #pragma unroll
     for (int i = 0; i < 2 * kBatch; ++i) {
-      const int r = min(r0 + i * kSelThreads, hi - 1);
+      const int r = r0 + i * kSelThreads;
+      if (r >= hi) break;
       const uint32_t k = weight_key(wv[i]);
-      if (cached) keys[r - lo + (r - lo) / kRun] = k;
+      if (cached) {
+        keys[r - lo] = k;
+        spos[r - lo] = pv[i];
+      }
       kmin = min(kmin, k);
       kmax = max(kmax, k);
       last = max(last, pv[i]);
@@ -274,9 +313,9 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
       int pv[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int r = min(r0 + i * C * kSelThreads, m - 1);
-        wv[i] = __ldcg(w + r);
-        pv[i] = __ldcg(pos + r);
+        const int r = r0 + i * C * kSelThreads;
+        wv[i] = r < m ? __ldcg(w + r) : 0.f;
+        pv[i] = r < m ? __ldcg(pos + r) : 0;
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
@@ -289,19 +328,20 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
   int cnt = 0;
   const int64_t from = (int64_t)last - a.n_recent;
   const bool guards = a.n_first + a.n_recent > 0;
-  // key of row r; `guard`: before the cached keys of guarded rows are marked
+  // key of row r, `guard`: for the first time (the cached keys of guarded rows are then marked)
   auto key = [&](int r, bool guard) {
-    uint32_t* kp = cached ? &keys[r - lo + (r - lo) / kRun] : nullptr;
-    uint32_t k = cached ? *kp : weight_key(__ldcg(w + r));
+    uint32_t k = cached ? keys[r - lo] : weight_key(__ldcg(w + r));
     if (guards && (guard || !cached)) {
-      const int p = __ldcg(pos + r);
+      const int p = cached ? spos[r - lo] : __ldcg(pos + r);
       if (p < a.n_first || p > from) {
         k = kGuarded;
-        if (cached) *kp = k;
+        if (cached) keys[r - lo] = k;
       }
     }
     return k;
   };
+  int32_t* hole = a.hole + bh * a.half;
+  int32_t* move = a.move + bh * a.half;
   if (m < n && m > 0 && n - m <= kFew) {
     // ---- the n - m least rows, the higher of equal ones first
     int drop[kFew];
@@ -309,19 +349,12 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
     for (int i = 0; i < kFew; ++i) {
       if (i >= n - m) break;
       uint64_t least = ~0ull;
-      for (int r0 = lo; r0 < hi; r0 += kBatch * kSelThreads) {
-        uint32_t kv[kBatch];
+      for (int r = lo + tid; r < hi; r += kSelThreads) {
+        uint64_t v = (uint64_t)key(r, i == 0) << 32 | (uint32_t)~r;
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) kv[j] = key(min(r0 + j * kSelThreads + tid, hi - 1), i == 0);
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const int r = min(r0 + j * kSelThreads + tid, hi - 1);
-          uint64_t v = (uint64_t)kv[j] << 32 | (uint32_t)~r;
-#pragma unroll
-          for (int d = 0; d < i; ++d)
-            if (drop[d] == r) v = ~0ull;
-          least = min(least, v);
-        }
+        for (int d = 0; d < i; ++d)
+          if (drop[d] == r) v = ~0ull;
+        least = min(least, v);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
@@ -340,37 +373,28 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
       drop[i] = (int)~(uint32_t)least;
     }
     // the k-th kept row at or past m goes to the k-th dropped row below m
-    if (rank == 0 && warp < n - m) {
+#pragma unroll
+    for (int i = 0; i < kFew; ++i) cnt += i < n - m && drop[i] < m;
+    if (rank == 0 && tid < 32) {
       auto dropped = [&](int r) {
         bool is = false;
 #pragma unroll
         for (int i = 0; i < kFew; ++i) is |= i < n - m && drop[i] == r;
         return is;
       };
-      int src = -1, dst = -1;
-      for (int r = m, k = 0; r < n; ++r)
-        if (!dropped(r) && k++ == warp) src = r;
+      // lane i < n - m: row m + i, and the i-th dropped row
+      int d = m;
 #pragma unroll
-      for (int i = 0; i < kFew; ++i) {
-        if (i >= n - m || drop[i] >= m) continue;
+      for (int i = 0; i < kFew; ++i)
+        if (lane == i && i < n - m) d = drop[i];
+      const bool is_move = lane < n - m && !dropped(m + lane), is_hole = lane < n - m && d < m;
+      const uint32_t moves = __ballot_sync(0xffffffffu, is_move);
+      if (is_move) move[__popc(moves & ((1u << lane) - 1))] = m + lane;
+      if (is_hole) {
         int below = 0;
 #pragma unroll
-        for (int d = 0; d < kFew; ++d) below += d < n - m && drop[d] < drop[i];
-        if (below == warp) dst = drop[i];
-      }
-      if (src >= 0 && dst >= 0) {
-        const int64_t ps = a.c.row(bh, src), pd = a.c.row(bh, dst);
-        if (ps >= 0 && pd >= 0)
-          for (int i = lane; i < 2 * a.words; i += 32) {
-            char* plane = i >= a.words ? a.c.v : a.c.k;
-            const int wd = i >= a.words ? i - a.words : i;
-            reinterpret_cast<uint4*>(plane + pd * a.words * 16)[wd] =
-                __ldcg(reinterpret_cast<const uint4*>(plane + ps * a.words * 16) + wd);
-          }
-        if (lane == 0) {
-          a.w_out[bh * a.cap + dst] = __ldcg(w + src);
-          a.pos_out[bh * a.cap + dst] = __ldcg(pos + src);
-        }
+        for (int i = 0; i < kFew; ++i) below += i < n - m && drop[i] < d;
+        hole[below] = d;
       }
     }
   } else if (m < n && m > 0) {
@@ -386,7 +410,10 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
       for (int r0 = lo; r0 < hi; r0 += kBatch * kSelThreads) {
         uint32_t kv[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) kv[i] = key(min(r0 + i * kSelThreads + tid, hi - 1), first);
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = r0 + i * kSelThreads + tid;
+          kv[i] = r < hi ? key(r, first) : 0u;
+        }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
           if (r0 + i * kSelThreads >= hi) break;
@@ -451,45 +478,60 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
       shift = max(0, shift - kBinBits);
       __syncthreads();  // found is read before the next round writes it
     }
-    // ---- holes and movers, in row order: rounds of kRun consecutive rows per thread
-    const int per_round = kSelThreads * kRun;
-    int32_t* hole = a.hole + bh * a.half;
-    int32_t* move = a.move + bh * a.half;
+    // ---- holes and movers, in row order: rounds of kRun consecutive rows per warp, 32 at a time
+    const int per_round = kSelWarps * kRun;
     int hole_at = 0, move_at = 0;
-    uint32_t hm = 0, mm = 0;  // holes and movers of this thread's run in the last round counted
+    uint32_t hm = 0, mm = 0;  // bit i: row i * 32 + lane of the warp's run, in the last round counted, is a hole (mover)
     int rk = 0;
     for (int pass = 0; pass < 2; ++pass) {
       int eq_at = eq_before, holes = hole_at, movers = move_at;
       for (int r0 = lo; r0 < hi; r0 += per_round) {
-        const int r = r0 + tid * kRun;
+        const int r = r0 + warp * kRun + lane;
         int all = 0;
         if (pass == 0 || run > per_round) {  // one round: the first pass has it all
           uint32_t keep = 0, eq = 0;
+          hm = mm = 0;
 #pragma unroll
-          for (int i = 0; i < kRun; ++i)
-            if (r + i < hi) {
-              const uint32_t k = key(r + i, false);
-              if (k > base || (!ties && k == base)) keep |= 1u << i;
-              if (k == base) eq |= 1u << i;
+          for (int i = 0; i < kRun / 32; ++i)
+            if (r + i * 32 < hi) {
+              const uint32_t k = key(r + i * 32, false);
+              keep |= (uint32_t)(k > base || (!ties && k == base)) << i;
+              eq |= (uint32_t)(k == base) << i;
             }
           if (ties) {
-            int left = need - eq_at - block_scan(__popc(eq), all, sm.scan);  // places for this thread's equal rows
+            int left = need - eq_at - warps_scan(__reduce_add_sync(0xffffffffu, __popc(eq)), all, sm.scan);
             eq_at += all;
-            for (; eq && left > 0; --left) {
-              keep |= eq & (0u - eq);
-              eq &= eq - 1;
+#pragma unroll
+            for (int i = 0; i < kRun / 32; ++i) {
+              const uint32_t b = __ballot_sync(0xffffffffu, eq >> i & 1);
+              if ((eq >> i & 1) && __popc(b & ((1u << lane) - 1)) < left) keep |= 1u << i;
+              left -= __popc(b);
             }
           }
-          const uint32_t in = r >= hi ? 0u : r + kRun <= hi ? 0xffffu : (1u << (hi - r)) - 1;
-          const uint32_t low = r >= m ? 0u : r + kRun <= m ? 0xffffu : (1u << (m - r)) - 1;
-          hm = in & low & ~keep;
-          mm = keep & ~low;
-          rk = block_scan(__popc(hm) | __popc(mm) << 16, all, sm.scan);
+#pragma unroll
+          for (int i = 0; i < kRun / 32; ++i) {
+            const int rr = r + i * 32;
+            if (rr >= hi) continue;
+            if (rr < m)
+              hm |= (~keep >> i & 1) << i;
+            else
+              mm |= (keep >> i & 1) << i;
+          }
+          rk = warps_scan(__reduce_add_sync(0xffffffffu, __popc(hm) | __popc(mm) << 16), all, sm.scan);
         }
         if (pass == 1) {
-          // (k < half unless the weights change under the call where their keys are read again and again)
-          for (int k = holes + (rk & 0xffff); hm && k < a.half; hm &= hm - 1) hole[k++] = r + __ffs(hm) - 1;
-          for (int k = movers + (rk >> 16); mm && k < a.half; mm &= mm - 1) move[k++] = r + __ffs(mm) - 1;
+          int h = holes + (rk & 0xffff), v = movers + (rk >> 16);
+          const uint32_t lower = (1u << lane) - 1;
+#pragma unroll
+          for (int i = 0; i < kRun / 32; ++i) {
+            // (h, v < half unless the weights change under the call where their keys are read again and again)
+            const uint32_t hb = __ballot_sync(0xffffffffu, hm >> i & 1), mb = __ballot_sync(0xffffffffu, mm >> i & 1);
+            const int hk = h + __popc(hb & lower), vk = v + __popc(mb & lower);
+            if ((hm >> i & 1) && hk < a.half) hole[hk] = r + i * 32;
+            if ((mm >> i & 1) && vk < a.half) move[vk] = r + i * 32;
+            h += __popc(hb);
+            v += __popc(mb);
+          }
         }
         holes += all & 0xffff;
         movers += all >> 16;
@@ -510,18 +552,24 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
         }
       }
     }
+    cnt = min(cnt, (int)a.half);
   }
   // (every access to another CTA's shared memory came before the last barrier that its owner passed)
+  if (all_here || n - m <= kFew) {
+    sync();  // the lists are written
+    constexpr int kRows = 4;
+    for (int i = (rank * kSelWarps + warp) * kRows; i < cnt; i += C * kSelWarps * kRows)
+      move_rows<kWords, kRows>(a, bh, i, min(kRows, cnt - i), lane);
+    cnt = 0;
+  }
   if (rank == 0 && tid == 0) {
-    a.count[bh] = min(cnt, (int)a.half);
+    a.count[bh] = cnt;
     a.lens_out[bh] = m;
   }
 }
 
-// Move the listed rows, kMoveRows of a pair to a warp: a lane looks up one
-// move, then the warp loads all rows' 16-byte words (K and V) before it stores
-// the first.  The pairs' counts form one list of such units that is cut evenly
-// over the warps of the grid.
+// Move the listed rows, kMoveRows of a pair to a warp.  The pairs' counts form
+// one list of such units that is cut evenly over the CTAs of the grid.
 constexpr int kMoveRows = 8;
 constexpr int kMoveThreads = 256;
 
@@ -571,22 +619,8 @@ __global__ void __launch_bounds__(kMoveThreads, 4) kv_move_kernel(const __grid_c
       s += (cnt + kMoveRows - 1) / kMoveRows;
       cnt = __ldcg(a.count + ++bh);
     }
-    const int i0 = (u - s) * kMoveRows, rows = min(kMoveRows, cnt - i0);
-    int64_t src = -1, dst = -1;
-    if (lane < rows) {
-      const int from = __ldcg(a.move + bh * a.half + i0 + lane), to = __ldcg(a.hole + bh * a.half + i0 + lane);
-      src = a.c.row(bh, from);
-      dst = a.c.row(bh, to);
-      a.w_out[bh * a.cap + to] = __ldcg(a.w + bh * a.cap + from);
-      a.pos_out[bh * a.cap + to] = __ldcg(a.pos + bh * a.cap + from);
-    }
-    // a row without a place is neither read nor written
-    if (src < 0 || dst < 0) src = 0, dst = -1;
-    __syncwarp();
-    copy_rows<kWords, kMoveRows>(
-        rows, lane,
-        [&](int k, bool is_v) { return (is_v ? a.c.v : a.c.k) + __shfl_sync(0xffffffffu, src, k) * (kWords * 8); },
-        [&](int k) { return __shfl_sync(0xffffffffu, dst, k); }, a.c);
+    const int i0 = (u - s) * kMoveRows;
+    move_rows<kWords, kMoveRows>(a, bh, i0, min(kMoveRows, cnt - i0), lane);
   }
 }
 
@@ -638,23 +672,26 @@ cudaError_t launch_kv_evict(const Plan& p, const KvView& c, const int32_t* budge
   a.hole = (int32_t*)((char*)ws + L.hole);
   a.move = (int32_t*)((char*)ws + L.move);
   a.half = c.max_len / 2;
-  a.words = p.cfg.d_h * p.esize / 16;
   // as many CTAs per pair as the SMs hold at once (one each), each with 1024 rows at least
   a.cluster = 1;
   while (a.cluster < kMaxCluster && (int64_t)a.BH * a.cluster * 2 <= kNumSMs && a.cluster * 2 * 1024 <= c.max_len)
     a.cluster *= 2;
-  const int run = (int)ceil_div64(ceil_div64(c.max_len, a.cluster), kRun) * kRun;
+  const int run = (int)ceil_div64(c.max_len, a.cluster);
   const int cached = run <= kSelCached;
-  const size_t smem = cached ? (size_t)(run + run / kRun) * 4 : 0;
-  static std::atomic<uint64_t> ready{0};
-  cudaError_t e = allow_smem((const void*)kv_select_kernel, (kSelCached + kSelCached / kRun) * 4, ready);
+  const size_t smem = cached ? (size_t)run * 8 : 0;
+  // at most half the rows move: no more than 512 per CTA, 4 us at worst, against 5 us on the host and the GPU for a
+  // second launch that most steps have no use for
+  const int all_here = run <= 1024;
+  const int words = p.cfg.d_h * p.esize / 8;
+  auto select = words == 16 ? kv_select_kernel<16> : words == 32 ? kv_select_kernel<32> : kv_select_kernel<64>;
+  static std::atomic<uint64_t> ready[3];
+  cudaError_t e = allow_smem((const void*)select, kSelCached * 8, ready[words == 16 ? 0 : words == 32 ? 1 : 2]);
   if (e != cudaSuccess) return e;
   {
     ProfScope ps(p, st, KID_KV_SELECT);
-    e = launch_pdl_cluster(kv_select_kernel, (unsigned)(a.BH * a.cluster), kSelThreads, a.cluster, smem, st, a, cached);
+    e = launch_pdl_cluster(select, (unsigned)(a.BH * a.cluster), kSelThreads, a.cluster, smem, st, a, cached, all_here);
   }
-  if (e != cudaSuccess) return e;
-  const int words = p.cfg.d_h * p.esize / 8;
+  if (e != cudaSuccess || all_here) return e;
   auto move = words == 16 ? kv_move_kernel<16> : words == 32 ? kv_move_kernel<32> : kv_move_kernel<64>;
   const int64_t most = a.BH * ceil_div64(a.half, kMoveRows * kMoveThreads / 32);
   ProfScope ps(p, st, KID_KV_MOVE);
