@@ -113,7 +113,7 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBinBits = 10;
 constexpr int kBins = 1 << kBinBits;
-constexpr int kRun = 512;             // consecutive rows per warp in the scan
+constexpr int kRun = 16;              // groups of 32 consecutive rows per warp in the scan, at most
 constexpr int kBatch = 4;             // rows per thread in flight
 constexpr int kSelCached = 24 * 1024; // rows per CTA whose keys and positions shared memory holds
 constexpr int kMaxCluster = 8;
@@ -478,52 +478,51 @@ __global__ void __launch_bounds__(kSelThreads)
       shift = max(0, shift - kBinBits);
       __syncthreads();  // found is read before the next round writes it
     }
-    // ---- holes and movers, in row order: rounds of kRun consecutive rows per warp, 32 at a time
-    const int per_round = kSelWarps * kRun;
+    // ---- holes and movers, in row order: rounds of `groups` times 32 consecutive rows per warp
+    const int groups = min(kRun, (run + kSelThreads - 1) / kSelThreads), per_round = groups * kSelThreads;
     int hole_at = 0, move_at = 0;
     uint32_t hm = 0, mm = 0;  // bit i: row i * 32 + lane of the warp's run, in the last round counted, is a hole (mover)
     int rk = 0;
     for (int pass = 0; pass < 2; ++pass) {
       int eq_at = eq_before, holes = hole_at, movers = move_at;
       for (int r0 = lo; r0 < hi; r0 += per_round) {
-        const int r = r0 + warp * kRun + lane;
+        const int r = r0 + warp * groups * 32 + lane;
         int all = 0;
         if (pass == 0 || run > per_round) {  // one round: the first pass has it all
-          uint32_t keep = 0, eq = 0;
+          uint32_t eq = 0;
           hm = mm = 0;
-#pragma unroll
-          for (int i = 0; i < kRun / 32; ++i)
-            if (r + i * 32 < hi) {
-              const uint32_t k = key(r + i * 32, false);
-              keep |= (uint32_t)(k > base || (!ties && k == base)) << i;
-              eq |= (uint32_t)(k == base) << i;
-            }
+#pragma unroll 2
+          for (int i = 0; i < groups; ++i) {
+            const int rr = r + i * 32;
+            if (rr >= hi) break;
+            const uint32_t k = key(rr, false);
+            const bool keep = k > base || (!ties && k == base);
+            hm |= (uint32_t)(rr < m && !keep) << i;
+            mm |= (uint32_t)(rr >= m && keep) << i;
+            eq |= (uint32_t)(k == base) << i;
+          }
           if (ties) {
             int left = need - eq_at - warps_scan(__reduce_add_sync(0xffffffffu, __popc(eq)), all, sm.scan);
             eq_at += all;
-#pragma unroll
-            for (int i = 0; i < kRun / 32; ++i) {
+#pragma unroll 1
+            for (int i = 0; i < groups; ++i) {
               const uint32_t b = __ballot_sync(0xffffffffu, eq >> i & 1);
-              if ((eq >> i & 1) && __popc(b & ((1u << lane) - 1)) < left) keep |= 1u << i;
+              if ((eq >> i & 1) && __popc(b & ((1u << lane) - 1)) < left) {  // kept after all
+                if (r + i * 32 < m)
+                  hm &= ~(1u << i);
+                else
+                  mm |= 1u << i;
+              }
               left -= __popc(b);
             }
-          }
-#pragma unroll
-          for (int i = 0; i < kRun / 32; ++i) {
-            const int rr = r + i * 32;
-            if (rr >= hi) continue;
-            if (rr < m)
-              hm |= (~keep >> i & 1) << i;
-            else
-              mm |= (keep >> i & 1) << i;
           }
           rk = warps_scan(__reduce_add_sync(0xffffffffu, __popc(hm) | __popc(mm) << 16), all, sm.scan);
         }
         if (pass == 1) {
           int h = holes + (rk & 0xffff), v = movers + (rk >> 16);
           const uint32_t lower = (1u << lane) - 1;
-#pragma unroll
-          for (int i = 0; i < kRun / 32; ++i) {
+#pragma unroll 2
+          for (int i = 0; i < groups; ++i) {
             // (h, v < half unless the weights change under the call where their keys are read again and again)
             const uint32_t hb = __ballot_sync(0xffffffffu, hm >> i & 1), mb = __ballot_sync(0xffffffffu, mm >> i & 1);
             const int hk = h + __popc(hb & lower), vk = v + __popc(mb & lower);
@@ -569,7 +568,9 @@ __global__ void __launch_bounds__(kSelThreads)
 }
 
 // Move the listed rows, kMoveRows of a pair to a warp.  The pairs' counts form
-// one list of such units that is cut evenly over the CTAs of the grid.
+// one list of such units that is cut evenly over the CTAs of the grid, four
+// times as many as run at once, so that an SM that gets less of the memory's
+// bandwidth takes fewer.
 constexpr int kMoveRows = 8;
 constexpr int kMoveThreads = 256;
 
@@ -679,9 +680,7 @@ cudaError_t launch_kv_evict(const Plan& p, const KvView& c, const int32_t* budge
   const int run = (int)ceil_div64(c.max_len, a.cluster);
   const int cached = run <= kSelCached;
   const size_t smem = cached ? (size_t)run * 8 : 0;
-  // at most half the rows move: no more than 512 per CTA, 4 us at worst, against 5 us on the host and the GPU for a
-  // second launch that most steps have no use for
-  const int all_here = run <= 1024;
+  const int all_here = run <= 2048;
   const int words = p.cfg.d_h * p.esize / 8;
   auto select = words == 16 ? kv_select_kernel<16> : words == 32 ? kv_select_kernel<32> : kv_select_kernel<64>;
   static std::atomic<uint64_t> ready[3];
@@ -695,7 +694,7 @@ cudaError_t launch_kv_evict(const Plan& p, const KvView& c, const int32_t* budge
   auto move = words == 16 ? kv_move_kernel<16> : words == 32 ? kv_move_kernel<32> : kv_move_kernel<64>;
   const int64_t most = a.BH * ceil_div64(a.half, kMoveRows * kMoveThreads / 32);
   ProfScope ps(p, st, KID_KV_MOVE);
-  return launch_pdl(move, (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, kNumSMs * 4)), kMoveThreads, 0, st, a);
+  return launch_pdl(move, (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, kNumSMs * 16)), kMoveThreads, 0, st, a);
 }
 
 }  // namespace dkv
