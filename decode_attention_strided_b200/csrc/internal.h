@@ -40,7 +40,7 @@ enum KernelId {
   KID_REFPACK = 0, KID_CAND_SIMT, KID_CAND_TC, KID_ENCODE_SIMT, KID_ENCODE_TC, KID_RECONSTRUCT, KID_DEC_REF,
   KID_DEC_PREP, KID_DEC_STREAM_SIMT, KID_DEC_STREAM_TC, KID_DEC_COMBINE, KID_DEC_FINAL,
   KID_APPEND_REFS, KID_APPEND_ROWS, KID_SPARSE_ATTEND, KID_SPARSE_MERGE, KID_SPARSE_SELECT,
-  KID_KV_APPEND, KID_KV_ATTEND, KID_KV_JOIN, KID_KV_WEIGHTS, KID_KV_SELECT, KID_KV_MOVE, KID_COUNT
+  KID_KV_APPEND, KID_KV_ATTEND, KID_KV_ATTEND_SHORT, KID_KV_JOIN, KID_KV_WEIGHTS, KID_KV_SELECT, KID_KV_MOVE, KID_COUNT
 };
 const char* kernel_name(int id);
 

@@ -18,6 +18,8 @@
 #include <atomic>
 #include <cmath>
 
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "sm100.cuh"
 
@@ -31,6 +33,14 @@ constexpr int kGroup = 16;         // rows of the smallest page
 constexpr int kSlotBytes = 8192;   // K or V rows of one unit of the split
 constexpr int kSlots = 3;          // of a warp's ring
 constexpr int kMinUnits = 4;       // a CTA gets at least these, or fewer CTAs work
+// A cluster per pair instead of the cut (one kernel instead of two): where its
+// CTAs find room at once (16 clusters of eight did not, 32 of four did) and take
+// 16 units at most.  bf16, d_h 128, four heads, us replayed, cluster / cut: 8
+// pairs of 513 rows 8.2 / 10.3, of 4096 (16 units a CTA) 12.3 / 14.4, of 8192
+// 18.6 / 18.4; 64 pairs of 1024 14.4 / 16.3; one pair of 8192 18.4 / 13.2.  Lengths
+// that differ cost the cluster more, the cut nothing, hence no more units.
+constexpr int kShortUnits = 16;
+constexpr int short_ctas(int cluster) { return cluster == 8 ? 96 : 128; }
 // rows per unit
 template <typename E, int DH>
 constexpr int kUnitRows = kSlotBytes / (DH * (int)sizeof(E));
@@ -957,6 +967,105 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
   in.drain();
 }
 
+// Short rows: a cluster per pair, its CTAs equal runs of the pair's units, the
+// parts joined through distributed shared memory and the weights added by the
+// CTA that has the rows, all in one kernel.  Bound by its chain of latencies
+// (length, page, rows, reduction, cluster barrier), not by bandwidth.
+template <int DH, typename Rows>
+__global__ void __launch_bounds__(kThreads, 1) kv_attend_short_kernel(const __grid_constant__ AttendArgs a, int C) {
+  namespace cg = cooperative_groups;
+  using E = typename Rows::E;
+  constexpr int kRows = kUnitRows<E, DH>;
+  extern __shared__ __align__(128) char smem_raw[];
+  auto& sm = *reinterpret_cast<AttendSmem<DH, Rows::GP>*>(smem_raw);
+  const cg::cluster_group cl = cg::this_cluster();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int bh = blockIdx.x / C, rank = blockIdx.x - bh * C;
+  init_ring(sm.ring, warp, lane);
+  __syncthreads();
+  sm100::grid_dep_wait();
+  sm100::grid_dep_launch();
+  const int raw = a.c.raw_len(bh), len = a.c.checked(raw);
+  if (rank == 0 && threadIdx.x == 0 && raw != len) a.c.report((uint32_t)raw);
+  const int ub = units_of(len, a.unit_log);
+  const int u0 = ub * rank / C, u1 = ub * (rank + 1) / C;
+  const Place at{bh, 0, len};
+  const Lens lens{a.c, sm.ring.lens, bh, a.unit_log};  // (no unit lies past this pair: the table is not read)
+  Loader<E, DH> in(lens, sm.ring, warp, lane, at, u0 + warp, u1);
+  for (int i = 0; i < kSlots; ++i) in.issue();
+  Rows rows;
+  rows.start(a, bh, lane);
+#pragma unroll 1
+  for (int u = u0 + warp; u < u1; u += kWarps) {
+    const int r = u * kRows;
+    float* xl = a.w ? a.logits + ((int64_t)bh * a.c.max_len + r) * a.G : nullptr;
+    rows.step(a, in, min(len - r, kRows), xl, lane);
+  }
+  if (!rows.finish(sm.merge, 0, warp, lane)) plain_rows(a, sm.merge, 0, at, u0 + warp, u1, warp, lane);
+  in.drain();
+  __syncthreads();
+  // this CTA's part, where the rows were: o[G][DH], m[kMaxG], l[kMaxG]
+  float* part = reinterpret_cast<float*>(sm.ring.ring);
+  const int cols = a.G * DH / 4;
+  if ((int)threadIdx.x < cols) {
+    const int g = threadIdx.x / (DH / 4), e = threadIdx.x % (DH / 4) * 4;
+    float m, l;
+    float4 o;
+    reduce_warps(sm.merge, 0, g, e, m, l, o);
+    *reinterpret_cast<float4*>(part + threadIdx.x * 4) = o;
+    if (e == 0) {
+      part[kMaxG * DH + g] = m;
+      part[kMaxG * DH + kMaxG + g] = l;
+    }
+  }
+  if (C == 1)
+    __syncthreads();
+  else
+    cl.sync();
+  auto peer = [&](int c) { return C == 1 ? part : cl.map_shared_rank(part, c); };
+  const int b = bh / a.H, h = bh - b * a.H;
+  for (int q = cols * rank / C + threadIdx.x; q < cols * (rank + 1) / C; q += kThreads) {
+    const int g = q / (DH / 4);
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < C; ++c) m = fmaxf(m, peer(c)[kMaxG * DH + g]);
+    const float mu = m == -INFINITY ? 0.f : m;
+    for (int c = 0; c < C; ++c) {
+      const float* p = peer(c);
+      const float f = exp2f(p[kMaxG * DH + g] - mu);
+      const float4 v = reinterpret_cast<const float4*>(p)[q];
+      l = fmaf(f, p[kMaxG * DH + kMaxG + g], l);
+      o.x = fmaf(f, v.x, o.x);
+      o.y = fmaf(f, v.y, o.y);
+      o.z = fmaf(f, v.z, o.z);
+      o.w = fmaf(f, v.w, o.w);
+    }
+    write_out<DH>(a, bh, b, h, g, q * 4 % DH, m, l, o);
+  }
+  if (a.w) {
+    float* L = part + kMaxG * DH + 2 * kMaxG;
+    if ((int)threadIdx.x < a.G) {
+      const int g = threadIdx.x;
+      float m = -INFINITY, l = 0.f;
+      for (int c = 0; c < C; ++c) m = fmaxf(m, peer(c)[kMaxG * DH + g]);
+      const float mu = m == -INFINITY ? 0.f : m;
+      for (int c = 0; c < C; ++c) l = fmaf(exp2f(peer(c)[kMaxG * DH + g] - mu), peer(c)[kMaxG * DH + kMaxG + g], l);
+      L[g] = m + log2f(l);
+    }
+    __syncthreads();
+    for (int r = u0 * kRows + threadIdx.x; r < min(len, u1 * kRows); r += kThreads) {
+      const float* x = a.logits + ((int64_t)bh * a.c.max_len + r) * a.G;
+      float* w = a.w + bh * a.cap + r;
+      const float old = *w;
+      float p = 0.f;
+      for (int g = 0; g < a.G; ++g)
+        if (L[g] != -INFINITY) p += exp2f(__ldcg(x + g) - L[g]);
+      *w = fmaf(a.decay, old, p);
+    }
+  }
+  if (C > 1) cl.sync();  // no CTA leaves while another reads its part
+}
+
 // Join the partial results.  CTA j looks at the cut between ranges j and j + 1:
 // where it falls inside a pair, that pair has np >= 2 parts and np - 1 such
 // cuts inside, and the CTA of cut i joins share i of the pair's G d_h outputs.
@@ -1085,7 +1194,16 @@ __global__ void __launch_bounds__(kThreads) kv_weights_kernel(const __grid_const
 }
 
 template <int DH, typename Rows>
-cudaError_t launch_t(const Plan& p, const AttendArgs& a, int grid, cudaStream_t st) {
+cudaError_t launch_t(const Plan& p, const AttendArgs& a, int grid, int cluster, cudaStream_t st) {
+  if (cluster) {
+    auto kern = kv_attend_short_kernel<DH, Rows>;
+    constexpr size_t smem = sizeof(AttendSmem<DH, Rows::GP>);
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = allow_smem((const void*)kern, smem, ready);
+    if (e != cudaSuccess) return e;
+    ProfScope ps(p, st, KID_KV_ATTEND_SHORT);
+    return launch_pdl_cluster(kern, (unsigned)(a.BH * cluster), kThreads, cluster, smem, st, a, cluster);
+  }
   auto kern = kv_attend_kernel<DH, Rows>;
   constexpr size_t smem = sizeof(AttendSmem<DH, Rows::GP>);
   static_assert(smem <= 227 * 1024, "shared memory of one CTA");
@@ -1112,16 +1230,16 @@ cudaError_t launch_t(const Plan& p, const AttendArgs& a, int grid, cudaStream_t 
 }
 
 template <int DH>
-cudaError_t launch_d(const Plan& p, const AttendArgs& a, int grid, cudaStream_t st) {
+cudaError_t launch_d(const Plan& p, const AttendArgs& a, int grid, int cluster, cudaStream_t st) {
   if (p.bf16) {
-    if (a.G <= 2) return launch_t<DH, Bf16Rows<DH, 2>>(p, a, grid, st);
-    if (a.G <= 4) return launch_t<DH, Bf16Rows<DH, 4>>(p, a, grid, st);
-    return launch_t<DH, Bf16Rows<DH, 8>>(p, a, grid, st);
+    if (a.G <= 2) return launch_t<DH, Bf16Rows<DH, 2>>(p, a, grid, cluster, st);
+    if (a.G <= 4) return launch_t<DH, Bf16Rows<DH, 4>>(p, a, grid, cluster, st);
+    return launch_t<DH, Bf16Rows<DH, 8>>(p, a, grid, cluster, st);
   }
-  if (a.G == 1) return launch_t<DH, F32Rows<DH, 1>>(p, a, grid, st);
-  if (a.G == 2) return launch_t<DH, F32Rows<DH, 2>>(p, a, grid, st);
-  if (a.G <= 4) return launch_t<DH, F32Rows<DH, 4>>(p, a, grid, st);
-  return launch_t<DH, F32Rows<DH, 8>>(p, a, grid, st);
+  if (a.G == 1) return launch_t<DH, F32Rows<DH, 1>>(p, a, grid, cluster, st);
+  if (a.G == 2) return launch_t<DH, F32Rows<DH, 2>>(p, a, grid, cluster, st);
+  if (a.G <= 4) return launch_t<DH, F32Rows<DH, 4>>(p, a, grid, cluster, st);
+  return launch_t<DH, F32Rows<DH, 8>>(p, a, grid, cluster, st);
 }
 
 }  // namespace
@@ -1155,7 +1273,13 @@ cudaError_t launch_kv_attend(const Plan& p, const KvView& c, const void* q, int6
   a.unit_log = unit == 64 ? 6 : unit == 32 ? 5 : 4;
   const int64_t most = a.BH * ceil_div64(c.max_len, unit);
   const int grid = (int)std::min<int64_t>(kKvMaxGrid, ceil_div64(most, kMinUnits));
-  return cfg.d_h == 128 ? launch_d<128>(p, a, grid, st) : launch_d<64>(p, a, grid, st);
+  // short rows (see kv_attend_short_kernel)
+  int cluster = 0;
+  const int64_t units = ceil_div64(c.max_len, unit);
+  for (int n = 1; n <= 8; n *= 2)
+    if ((int64_t)a.BH * n <= short_ctas(n)) cluster = n;
+  if (cluster && units > (int64_t)cluster * kShortUnits) cluster = 0;
+  return cfg.d_h == 128 ? launch_d<128>(p, a, grid, cluster, st) : launch_d<64>(p, a, grid, cluster, st);
 }
 
 }  // namespace dkv

@@ -30,7 +30,7 @@ const char* kernel_name(int id) {
       "refpack", "candidates_simt", "candidates_tc", "encode_simt", "encode_tc", "reconstruct",
       "decode_ref", "decode_prep", "decode_stream_simt", "decode_stream_tc", "decode_combine", "decode_final",
       "append_refs", "append_rows", "sparse_attend", "sparse_merge", "sparse_select",
-      "kv_append", "kv_attend", "kv_join", "kv_weights", "kv_select", "kv_move"};
+      "kv_append", "kv_attend", "kv_attend_short", "kv_join", "kv_weights", "kv_select", "kv_move"};
   return (id >= 0 && id < KID_COUNT) ? names[id] : "?";
 }
 
