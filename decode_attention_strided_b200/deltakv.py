@@ -406,36 +406,31 @@ def _kv_tensor(name, t, dtype, shape, dev):
     or device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor")
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)}, got {t.dtype} {list(t.shape)}"
-                         f"{'' if t.is_contiguous() else ' (not contiguous)'}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, not with the cache")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} where the cache is, got {t.dtype} "
+                     f"{list(t.shape)}{'' if t.is_contiguous() else ' (not contiguous)'} on {t.device}")
 
 
-def _kv_meta(name, t, dtype, p, dev):
+def _kv_meta(name, t, dtype, pairs, dev):
     """A [B, H, cap] array of row weights or positions: (pointer, cap)."""
     if not isinstance(t, torch.Tensor) or t.dim() != 3:
-        raise ValueError(f"{name} must be a tensor [{p.cfg.batch}, {p.cfg.kv_heads}, cap]")
+        raise ValueError(f"{name} must be a tensor {list(pairs) + ['cap']}")
     cap = t.shape[2]
-    return _kv_tensor(name, t, dtype, (p.cfg.batch, p.cfg.kv_heads, cap), dev), cap
+    return _kv_tensor(name, t, dtype, (*pairs, cap), dev), cap
 
 
 def _kv_rows(name, t, dtype, shape, dev):
-    """The data pointer of a tensor with any strides but the last dimension's."""
+    """Strides, in elements, of a tensor that is contiguous in its last
+    dimension only.  (torch leaves the stride of a dimension of one element
+    arbitrary; it is never used, so the callers pass 0 for it.)"""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor")
-    if t.dtype is not dtype or t.shape != shape or t.stride(-1) != 1 or t.get_device() != dev:
+    st = t.stride()
+    if t.dtype is not dtype or t.shape != shape or st[-1] != 1 or t.get_device() != dev:
         raise ValueError(f"{name} must be {dtype} {list(shape)}, contiguous in its last dimension, where the cache "
-                         f"is; got {t.dtype} {list(t.shape)}, strides {t.stride()}, on {t.device}")
-    return t.data_ptr()
-
-
-def _stride(t, i, one=0):
-    """Stride of dimension i; `one` where it has one element, whose stride
-    (torch leaves it arbitrary) is never used."""
-    return t.stride(i) if t.shape[i] > 1 else one
+                         f"is; got {t.dtype} {list(t.shape)}, strides {st}, on {t.device}")
+    return st
 
 
 class KVCache:
@@ -483,28 +478,27 @@ def kv_append(p: Plan, cache: KVCache, max_len: int, K, V, workspace, n_tokens=N
     sequence brings (default n_new).  pos int32 and weights float32 [B, H, cap]
     get first_pos[b] + t and token_weights [B, H, n_new] (0 where None)."""
     c, dev = p.cfg, cache.dev
-    B, H = c.batch, c.kv_heads
+    B, H, d = c.batch, c.kv_heads, c.d_h
     if not isinstance(K, torch.Tensor) or K.dim() != 4:
-        raise ValueError(f"K and V must have shape [{B}, {H}, n_new, {c.d_h}]")
+        raise ValueError(f"K and V must have shape [{B}, {H}, n_new, {d}]")
     n_new = K.shape[2]
-    shape, dt = (B, H, n_new, c.d_h), c.torch_dtype()
-    kp, vp = _kv_rows("K", K, dt, shape, dev), _kv_rows("V", V, dt, shape, dev)
-    if n_new == 0:
-        return
-    ks = (_stride(K, 0), _stride(K, 1), _stride(K, 2, c.d_h))
-    if ks != (_stride(V, 0), _stride(V, 1), _stride(V, 2, c.d_h)):
+    shape, dt = (B, H, n_new, d), c.torch_dtype()
+    ks, vs = _kv_rows("K", K, dt, shape, dev), _kv_rows("V", V, dt, shape, dev)
+    if ks != vs and any(a != b for a, b, n in zip(ks, vs, shape) if n > 1):
         raise ValueError("K and V must share strides")
     nt = None if n_tokens is None else _kv_tensor("n_tokens", n_tokens, torch.int32, (B,), dev)
     fp = None if first_pos is None else _kv_tensor("first_pos", first_pos, torch.int32, (B,), dev)
-    tw = None if token_weights is None else _kv_tensor("token_weights", token_weights, torch.float32, (B, H, n_new),
-                                                       dev)
-    w, cap = (None, 0) if weights is None else _kv_meta("weights", weights, torch.float32, p, dev)
-    pp, cap_p = (None, cap) if pos is None else _kv_meta("pos", pos, torch.int32, p, dev)
+    tw = None if token_weights is None else _kv_tensor("token_weights", token_weights, torch.float32, shape[:3], dev)
+    w, cap = (None, 0) if weights is None else _kv_meta("weights", weights, torch.float32, (B, H), dev)
+    pp, cap_p = (None, cap) if pos is None else _kv_meta("pos", pos, torch.int32, (B, H), dev)
     if w is not None and cap != cap_p:
         raise ValueError(f"weights and pos must have the same cap, got {cap} and {cap_p}")
     view, ws, nbytes, st = cache._call(p, max_len, workspace, stream)
-    _check("deltakv_kv_append", _lib.deltakv_kv_append(
-        p.handle, view, n_new, kp, vp, _I3(*ks), nt, fp, w, pp, cap_p, tw, ws, nbytes, st))
+    code = _lib.deltakv_kv_append(p.handle, view, n_new, K.data_ptr(), V.data_ptr(),
+                                  _I3(ks[0] if B > 1 else 0, ks[1] if H > 1 else 0, ks[2] if n_new > 1 else d), nt, fp,
+                                  w, pp, cap_p, tw, ws, nbytes, st)
+    if code:
+        _check("deltakv_kv_append", code)
 
 
 def kv_decode_attention(p: Plan, cache: KVCache, max_len: int, q, out, workspace, weights=None, decay: float = 1.0,
@@ -514,14 +508,17 @@ def kv_decode_attention(p: Plan, cache: KVCache, max_len: int, q, out, workspace
     row's attention weight (decay w + p)."""
     c, dev = p.cfg, cache.dev
     shape = (c.batch, c.q_heads, c.d_h)
-    qp = _kv_rows("q", q, c.torch_dtype(), shape, dev)
-    op = _kv_rows("out", out, torch.float32, shape, dev)
-    w, cap = (None, 0) if weights is None else _kv_meta("weights", weights, torch.float32, p, dev)
+    qs = _kv_rows("q", q, c.torch_dtype(), shape, dev)
+    os_ = _kv_rows("out", out, torch.float32, shape, dev)
+    w, cap = (None, 0) if weights is None else _kv_meta("weights", weights, torch.float32, (c.batch, c.kv_heads), dev)
     lp = None if lse is None else _kv_tensor("lse", lse, torch.float32, shape[:2], dev)
     view, ws, nbytes, st = cache._call(p, max_len, workspace, stream)
-    _check("deltakv_kv_decode_attention", _lib.deltakv_kv_decode_attention(
-        p.handle, view, qp, _I2(_stride(q, 0), _stride(q, 1)), op, _I2(_stride(out, 0), _stride(out, 1)), lp, w, cap,
-        decay, ws, nbytes, st))
+    many, heads = c.batch > 1, c.q_heads > 1
+    code = _lib.deltakv_kv_decode_attention(
+        p.handle, view, q.data_ptr(), _I2(qs[0] if many else 0, qs[1] if heads else 0), out.data_ptr(),
+        _I2(os_[0] if many else 0, os_[1] if heads else 0), lp, w, cap, decay, ws, nbytes, st)
+    if code:
+        _check("deltakv_kv_decode_attention", code)
 
 
 def kv_evict(p: Plan, cache: KVCache, max_len: int, budget, weights, pos, workspace, n_first: int = 0,
@@ -532,7 +529,7 @@ def kv_evict(p: Plan, cache: KVCache, max_len: int, budget, weights, pos, worksp
     cache.lens, weights and pos (in place)."""
     dev = cache.dev
     pairs = (p.cfg.batch, p.cfg.kv_heads)
-    w, cap = _kv_meta("weights", weights, torch.float32, p, dev)
+    w, cap = _kv_meta("weights", weights, torch.float32, pairs, dev)
     shape = (*pairs, cap)
     pp = _kv_tensor("pos", pos, torch.int32, shape, dev)
     wo = w if weights_out is None else _kv_tensor("weights_out", weights_out, torch.float32, shape, dev)
@@ -540,8 +537,9 @@ def kv_evict(p: Plan, cache: KVCache, max_len: int, budget, weights, pos, worksp
     bp = _kv_tensor("budget", budget, torch.int32, pairs, dev)
     lo = _kv_tensor("lens_out", cache.lens if lens_out is None else lens_out, torch.int32, pairs, dev)
     view, ws, nbytes, st = cache._call(p, max_len, workspace, stream)
-    _check("deltakv_kv_evict", _lib.deltakv_kv_evict(
-        p.handle, view, bp, n_first, n_recent, w, pp, wo, po, cap, lo, ws, nbytes, st))
+    code = _lib.deltakv_kv_evict(p.handle, view, bp, n_first, n_recent, w, pp, wo, po, cap, lo, ws, nbytes, st)
+    if code:
+        _check("deltakv_kv_evict", code)
 
 
 def reconstruct(p: Plan, T: int, cache, W3, b3, W4, b4, K_out, V_out, workspace, stream=None):
