@@ -95,17 +95,17 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) kv_append_kernel(const _
 
 // ---- evict
 // A cluster of CTAs per pair, each with a run of its rows.  Weights become
-// integer keys that order like them (kept in shared memory where they fit),
-// and the m-th largest key is found by narrowing a range of keys: 1024 equal
-// bins over it, counted per CTA and added up over the cluster through
-// distributed shared memory, until the bin that holds the m-th key is kept
-// whole or holds one key only; two rounds as a rule, three or four at most.
-// (A cache held at its budget drops a row or so per token: up to kFew rows are
-// found as that many minima instead, and moved at once.)
-// Rows above the threshold and the first of those equal to it are kept; a scan
-// in row order numbers the dropped rows below m (holes) and the kept rows at or
-// past m (movers), of which there are equally many: mover i goes to hole i.
-// Bound by its chain of block and cluster barriers: the keys are read once.
+// integer keys that order like them, held in registers (runs of more than 16
+// rows a thread are read again for each step instead).  The m-th largest key is
+// found by narrowing a range of keys: 1024 equal bins over it, counted per CTA
+// and added up over the cluster through distributed shared memory, until the
+// bin that holds the m-th key is kept whole or holds one key only; two rounds
+// as a rule, four at most.  (A cache held at its budget drops a row or so per
+// token: up to kFew rows are found as that many minima instead.)  Rows above
+// the threshold and the first of those equal to it are kept; a scan in row
+// order numbers the dropped rows below m (holes) and the kept rows at or past m
+// (movers), of which there are equally many: mover i goes to hole i.  Bound by
+// its chain of block and cluster barriers: the keys are read once.
 // Where the moves are few for certain, the clusters make them; else a second
 // kernel does, spread over the whole GPU whatever the pairs' shares: bound by
 // the rows read and written.
@@ -113,9 +113,7 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBinBits = 10;
 constexpr int kBins = 1 << kBinBits;
-constexpr int kRun = 16;              // groups of 32 consecutive rows per warp in the scan, at most
-constexpr int kBatch = 4;             // rows per thread in flight
-constexpr int kSelCached = 24 * 1024; // rows per CTA whose keys and positions shared memory holds
+constexpr int kPerSmall = 2, kPerLarge = 16;  // rows per thread in registers
 constexpr int kMaxCluster = 8;
 constexpr int kFew = 4;               // this many rows to drop are found one by one
 static_assert(kBins == kSelThreads && kSelWarps == 32, "a thread per bin, a lane per warp");
@@ -170,17 +168,6 @@ __device__ __forceinline__ int block_scan(int v, int& all, int* sh) {
   return __shfl_sync(0xffffffffu, ti - t, warp) + inc - v;
 }
 
-// The same for a value that is the warp's, not the thread's.
-__device__ __forceinline__ int warps_scan(int v, int& all, int* sh) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __syncthreads();
-  if (lane == 0) sh[warp] = v;
-  __syncthreads();
-  const int t = sh[lane];
-  all = __reduce_add_sync(0xffffffffu, t);
-  return __reduce_add_sync(0xffffffffu, lane < warp ? t : 0);
-}
-
 // What a CTA tells the others of its cluster.
 struct SelExchange {
   uint32_t kmin, kmax;
@@ -193,6 +180,7 @@ struct SelSmem {
   int hist[2][kBins + 1];  // bin kBins: guarded rows
   SelExchange from[kMaxCluster]; // written by the CTAs of the cluster
   int scan[32];
+  int at[kPerLarge * kSelWarps];  // rows of 32 rows (a warp's): counts, then their prefix
   uint32_t rmin[kSelWarps], rmax[kSelWarps];
   int rlast[kSelWarps];
   uint64_t rleast[kSelWarps];
@@ -218,13 +206,24 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, int bh, int i0, in
       [&](int k) { return __shfl_sync(0xffffffffu, dst, k); }, a.c);
 }
 
-// cached: the rows' keys and positions fit shared memory; all_here: the
-// clusters make all moves, not the few of a step alone.
-template <int kWords>
-__global__ void __launch_bounds__(kSelThreads)
-    kv_select_kernel(const __grid_constant__ EvictArgs a, int cached, int all_here) {
+// Exclusive prefix over sm.at's first N entries, in place; the total.
+template <int N>
+__device__ __forceinline__ int scan_counts(SelSmem& sm) {
+  __syncthreads();
+  const int i = threadIdx.x;
+  int all;
+  const int pre = block_scan(i < N ? sm.at[i] : 0, all, sm.scan);
+  if (i < N) sm.at[i] = pre;
+  __syncthreads();
+  return all;
+}
+
+// kPer: rows per thread in registers; kWords: words of a row for the clusters
+// to make the moves themselves, or 0.
+template <int kPer, int kWords>
+__global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_constant__ EvictArgs a) {
   namespace cg = cooperative_groups;
-  extern __shared__ uint32_t keys[];  // [run], then the positions
+  constexpr int kChunk = kPer * kSelThreads;
   __shared__ SelSmem sm;
   const cg::cluster_group cl = cg::this_cluster();
   const int C = a.cluster, rank = C == 1 ? 0 : (int)cl.block_rank();
@@ -246,32 +245,33 @@ __global__ void __launch_bounds__(kSelThreads)
     else
       cl.sync();
   };
-  // ---- keys of this CTA's rows, their range, the largest position, and the pages
+  auto peer = [&](auto* p, int c) { return C == 1 ? p : cl.map_shared_rank(p, c); };
+  // ---- keys and positions of rows r0 + j kSelThreads + tid, their range, the largest position, and the pages
+  const bool resident = run <= kChunk;
+  uint32_t key[kPer];
+  int ps[kPer];
+  auto load = [&](int r0) {
+    float wv[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int r = r0 + j * kSelThreads + tid;
+      wv[j] = r < hi ? __ldcg(w + r) : 0.f;
+      ps[j] = r < hi ? __ldcg(pos + r) : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) key[j] = weight_key(wv[j]);
+  };
   uint32_t kmin = 0xffffffffu, kmax = 0u;
   int last = INT32_MIN, bad = 0;
-  int* spos = reinterpret_cast<int*>(keys) + run;
-  for (int r0 = lo + tid; r0 < hi; r0 += 2 * kBatch * kSelThreads) {
-    float wv[2 * kBatch];
-    int pv[2 * kBatch];
+  for (int r0 = lo; r0 < hi; r0 += kChunk) {
+    load(r0);
 #pragma unroll
-    for (int i = 0; i < 2 * kBatch; ++i) {
-      const int r = r0 + i * kSelThreads;
-      wv[i] = r < hi ? __ldcg(w + r) : 0.f;
-      pv[i] = r < hi ? __ldcg(pos + r) : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < 2 * kBatch; ++i) {
-      const int r = r0 + i * kSelThreads;
-      if (r >= hi) break;
-      const uint32_t k = weight_key(wv[i]);
-      if (cached) {
-        keys[r - lo] = k;
-        spos[r - lo] = pv[i];
+    for (int j = 0; j < kPer; ++j)
+      if (r0 + j * kSelThreads + tid < hi) {
+        kmin = min(kmin, key[j]);
+        kmax = max(kmax, key[j]);
+        last = max(last, ps[j]);
       }
-      kmin = min(kmin, k);
-      kmax = max(kmax, k);
-      last = max(last, pv[i]);
-    }
   }
   // the pages of the rows this CTA starts with
   for (int r = ((lo >> a.c.page_log) + tid) << a.c.page_log; r < hi; r += kSelThreads << a.c.page_log)
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kSelThreads)
     kmax = __reduce_max_sync(0xffffffffu, sm.rmax[lane]);
     last = __reduce_max_sync(0xffffffffu, sm.rlast[lane]);
     if (lane < C) {
-      SelExchange* to = C == 1 ? &sm.from[0] : cl.map_shared_rank(&sm.from[rank], lane);
+      SelExchange* to = peer(&sm.from[C == 1 ? 0 : rank], lane);
       to->kmin = kmin;
       to->kmax = kmax;
       to->last = last;
@@ -308,40 +308,33 @@ __global__ void __launch_bounds__(kSelThreads)
   if (bad || budget < 0) m = n;
   // rows below m start out as themselves; the move writes over the holes
   if (a.w_out != a.w || a.pos_out != a.pos) {
-    for (int r0 = rank * kSelThreads + tid; r0 < m; r0 += kBatch * C * kSelThreads) {
-      float wv[kBatch];
-      int pv[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int r = r0 + i * C * kSelThreads;
-        wv[i] = r < m ? __ldcg(w + r) : 0.f;
-        pv[i] = r < m ? __ldcg(pos + r) : 0;
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int r = r0 + i * C * kSelThreads;
-        if (r < m && a.w_out != a.w) a.w_out[bh * a.cap + r] = wv[i];
-        if (r < m && a.pos_out != a.pos) a.pos_out[bh * a.cap + r] = pv[i];
-      }
+#pragma unroll 4
+    for (int r = rank * kSelThreads + tid; r < m; r += C * kSelThreads) {
+      const float wv = __ldcg(w + r);
+      const int pv = __ldcg(pos + r);
+      if (a.w_out != a.w) a.w_out[bh * a.cap + r] = wv;
+      if (a.pos_out != a.pos) a.pos_out[bh * a.cap + r] = pv;
     }
   }
   int cnt = 0;
   const int64_t from = (int64_t)last - a.n_recent;
   const bool guards = a.n_first + a.n_recent > 0;
-  // key of row r, `guard`: for the first time (the cached keys of guarded rows are then marked)
-  auto key = [&](int r, bool guard) {
-    uint32_t k = cached ? keys[r - lo] : weight_key(__ldcg(w + r));
-    if (guards && (guard || !cached)) {
-      const int p = cached ? spos[r - lo] : __ldcg(pos + r);
-      if (p < a.n_first || p > from) {
-        k = kGuarded;
-        if (cached) keys[r - lo] = k;
-      }
-    }
-    return k;
+  auto mark = [&] {
+    if (guards)
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (ps[j] < a.n_first || ps[j] > from) key[j] = kGuarded;
   };
+  // the keys of a chunk, guarded rows marked
+  auto fetch = [&](int r0) {
+    if (resident) return;
+    load(r0);
+    mark();
+  };
+  if (resident) mark();
   int32_t* hole = a.hole + bh * a.half;
   int32_t* move = a.move + bh * a.half;
+  const uint32_t lower = (1u << lane) - 1;
   if (m < n && m > 0 && n - m <= kFew) {
     // ---- the n - m least rows, the higher of equal ones first
     int drop[kFew];
@@ -349,12 +342,16 @@ __global__ void __launch_bounds__(kSelThreads)
     for (int i = 0; i < kFew; ++i) {
       if (i >= n - m) break;
       uint64_t least = ~0ull;
-      for (int r = lo + tid; r < hi; r += kSelThreads) {
-        uint64_t v = (uint64_t)key(r, i == 0) << 32 | (uint32_t)~r;
+      for (int r0 = lo; r0 < hi; r0 += kChunk) {
+        fetch(r0);
 #pragma unroll
-        for (int d = 0; d < i; ++d)
-          if (drop[d] == r) v = ~0ull;
-        least = min(least, v);
+        for (int j = 0; j < kPer; ++j) {
+          const int r = r0 + j * kSelThreads + tid;
+          bool in = r < hi;
+#pragma unroll
+          for (int d = 0; d < i; ++d) in &= drop[d] != r;
+          if (in) least = min(least, (uint64_t)key[j] << 32 | (uint32_t)~r);
+        }
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
@@ -365,7 +362,7 @@ __global__ void __launch_bounds__(kSelThreads)
         least = sm.rleast[lane];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
-        if (lane < C) (C == 1 ? &sm.from[0] : cl.map_shared_rank(&sm.from[rank], lane))->least[i] = least;
+        if (lane < C) peer(&sm.from[C == 1 ? 0 : rank], lane)->least[i] = least;
       }
       sync();
       least = sm.from[0].least[i];
@@ -376,26 +373,21 @@ __global__ void __launch_bounds__(kSelThreads)
 #pragma unroll
     for (int i = 0; i < kFew; ++i) cnt += i < n - m && drop[i] < m;
     if (rank == 0 && tid < 32) {
-      auto dropped = [&](int r) {
-        bool is = false;
-#pragma unroll
-        for (int i = 0; i < kFew; ++i) is |= i < n - m && drop[i] == r;
-        return is;
-      };
       // lane i < n - m: row m + i, and the i-th dropped row
-      int d = m;
+      int d = m, below = 0;
+      bool dropped = false;
 #pragma unroll
       for (int i = 0; i < kFew; ++i)
-        if (lane == i && i < n - m) d = drop[i];
-      const bool is_move = lane < n - m && !dropped(m + lane), is_hole = lane < n - m && d < m;
-      const uint32_t moves = __ballot_sync(0xffffffffu, is_move);
-      if (is_move) move[__popc(moves & ((1u << lane) - 1))] = m + lane;
-      if (is_hole) {
-        int below = 0;
+        if (i < n - m) {
+          dropped |= drop[i] == m + lane;
+          if (lane == i) d = drop[i];
+        }
 #pragma unroll
-        for (int i = 0; i < kFew; ++i) below += i < n - m && drop[i] < d;
-        hole[below] = d;
-      }
+      for (int i = 0; i < kFew; ++i) below += i < n - m && drop[i] < d;
+      const bool is_move = lane < n - m && !dropped;
+      const uint32_t moves = __ballot_sync(0xffffffffu, is_move);
+      if (is_move) move[__popc(moves & lower)] = m + lane;
+      if (lane < n - m && d < m) hole[below] = d;
     }
   } else if (m < n && m > 0) {
     // ---- the threshold: keys in [base, base + span] are in question, `need` of them are kept
@@ -407,19 +399,14 @@ __global__ void __launch_bounds__(kSelThreads)
       int* hist = sm.hist[buf];
       for (int i = tid; i <= kBins; i += kSelThreads) hist[i] = 0;
       __syncthreads();
-      for (int r0 = lo; r0 < hi; r0 += kBatch * kSelThreads) {
-        uint32_t kv[kBatch];
+      for (int r0 = lo; r0 < hi; r0 += kChunk) {
+        fetch(r0);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int r = r0 + i * kSelThreads + tid;
-          kv[i] = r < hi ? key(r, first) : 0u;
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          if (r0 + i * kSelThreads >= hi) break;
-          const uint32_t k = kv[i], d = k - base;
+        for (int j = 0; j < kPer; ++j) {
+          if (r0 + j * kSelThreads >= hi) break;
+          const uint32_t k = key[j], d = k - base;
           int bin = -1;
-          if (r0 + i * kSelThreads + tid < hi) {
+          if (r0 + j * kSelThreads + tid < hi) {
             if (k == kGuarded)
               bin = first ? kBins : -1;
             else if (k >= base && d <= span)
@@ -436,24 +423,18 @@ __global__ void __launch_bounds__(kSelThreads)
       }
       sync();
       // add up the cluster's counts: thread t has bin kBins - 1 - t (largest keys first)
-      int sum = 0, guard = 0;
-      {
-        int got[kMaxCluster];
+      int got[kMaxCluster], sum = 0;
 #pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c)
-          got[c] = c < C ? (C == 1 ? hist : cl.map_shared_rank(hist, c))[kBins - 1 - tid] : 0;
-        int gv = 0;
-        if (first && lane < C) gv = (C == 1 ? hist : cl.map_shared_rank(hist, lane))[kBins];
-        guard = __reduce_add_sync(0xffffffffu, gv);
+      for (int c = 0; c < kMaxCluster; ++c) got[c] = c < C ? peer(hist, c)[kBins - 1 - tid] : 0;
+      const int guard = __reduce_add_sync(0xffffffffu, first && lane < C ? peer(hist, lane)[kBins] : 0);
 #pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) sum += got[c];
-      }
+      for (int c = 0; c < kMaxCluster; ++c) sum += got[c];
       if (first && guard >= m) {
         // the guarded rows alone fill the budget (equal positions): the first of them are kept
         base = kGuarded;
         ties = guard > m;
         need = m;
-        for (int c = 0; c < rank; ++c) eq_before += (C == 1 ? hist : cl.map_shared_rank(hist, c))[kBins];
+        for (int c = 0; c < rank; ++c) eq_before += peer(hist, c)[kBins];
         break;
       }
       need -= guard;
@@ -471,73 +452,77 @@ __global__ void __launch_bounds__(kSelThreads)
       if (count == need || shift == 0) {
         ties = count != need;
         if (ties)
-          for (int c = 0; c < rank; ++c) eq_before += (C == 1 ? hist : cl.map_shared_rank(hist, c))[bin];
+          for (int c = 0; c < rank; ++c) eq_before += peer(hist, c)[bin];
         break;
       }
       span = (1u << shift) - 1;
       shift = max(0, shift - kBinBits);
       __syncthreads();  // found is read before the next round writes it
     }
-    // ---- holes and movers, in row order: rounds of `groups` times 32 consecutive rows per warp
-    const int groups = min(kRun, (run + kSelThreads - 1) / kSelThreads), per_round = groups * kSelThreads;
+    // ---- holes and movers, in row order: 32 rows (a warp's) at a time
     int hole_at = 0, move_at = 0;
-    uint32_t hm = 0, mm = 0;  // bit i: row i * 32 + lane of the warp's run, in the last round counted, is a hole (mover)
-    int rk = 0;
+    uint32_t hm = 0, mm = 0;  // bit j: the thread's j-th row of the last chunk counted is a hole (mover)
     for (int pass = 0; pass < 2; ++pass) {
       int eq_at = eq_before, holes = hole_at, movers = move_at;
-      for (int r0 = lo; r0 < hi; r0 += per_round) {
-        const int r = r0 + warp * groups * 32 + lane;
+      for (int r0 = lo; r0 < hi; r0 += kChunk) {
         int all = 0;
-        if (pass == 0 || run > per_round) {  // one round: the first pass has it all
+        if (pass == 0 || !resident) {  // (of a single chunk, the first pass has it all)
+          fetch(r0);
           uint32_t eq = 0;
           hm = mm = 0;
-#pragma unroll 2
-          for (int i = 0; i < groups; ++i) {
-            const int rr = r + i * 32;
-            if (rr >= hi) break;
-            const uint32_t k = key(rr, false);
-            const bool keep = k > base || (!ties && k == base);
-            hm |= (uint32_t)(rr < m && !keep) << i;
-            mm |= (uint32_t)(rr >= m && keep) << i;
-            eq |= (uint32_t)(k == base) << i;
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            const int r = r0 + j * kSelThreads + tid;
+            const bool in = r < hi, keep = key[j] > base || (!ties && key[j] == base);
+            hm |= (uint32_t)(in && r < m && !keep) << j;
+            mm |= (uint32_t)(in && r >= m && keep) << j;
+            eq |= (uint32_t)(in && key[j] == base) << j;
           }
           if (ties) {
-            int left = need - eq_at - warps_scan(__reduce_add_sync(0xffffffffu, __popc(eq)), all, sm.scan);
-            eq_at += all;
-#pragma unroll 1
-            for (int i = 0; i < groups; ++i) {
-              const uint32_t b = __ballot_sync(0xffffffffu, eq >> i & 1);
-              if ((eq >> i & 1) && __popc(b & ((1u << lane) - 1)) < left) {  // kept after all
-                if (r + i * 32 < m)
-                  hm &= ~(1u << i);
-                else
-                  mm |= 1u << i;
-              }
-              left -= __popc(b);
+#pragma unroll 2
+            for (int j = 0; j < kPer; ++j) {
+              const uint32_t b = __ballot_sync(0xffffffffu, eq >> j & 1);
+              if (lane == 0) sm.at[j * kSelWarps + warp] = __popc(b);
             }
+            all = scan_counts<kPer * kSelWarps>(sm);
+#pragma unroll 2
+            for (int j = 0; j < kPer; ++j) {
+              const uint32_t b = __ballot_sync(0xffffffffu, eq >> j & 1);
+              if ((eq >> j & 1) && eq_at + sm.at[j * kSelWarps + warp] + __popc(b & lower) < need) {  // kept after all
+                if (r0 + j * kSelThreads + tid < m)
+                  hm &= ~(1u << j);
+                else
+                  mm |= 1u << j;
+              }
+            }
+            eq_at += all;
+            __syncthreads();
           }
-          rk = warps_scan(__reduce_add_sync(0xffffffffu, __popc(hm) | __popc(mm) << 16), all, sm.scan);
+#pragma unroll 2
+          for (int j = 0; j < kPer; ++j) {
+            const uint32_t hb = __ballot_sync(0xffffffffu, hm >> j & 1), mb = __ballot_sync(0xffffffffu, mm >> j & 1);
+            if (lane == 0) sm.at[j * kSelWarps + warp] = __popc(hb) | __popc(mb) << 16;
+          }
+          all = scan_counts<kPer * kSelWarps>(sm);
         }
         if (pass == 1) {
-          int h = holes + (rk & 0xffff), v = movers + (rk >> 16);
-          const uint32_t lower = (1u << lane) - 1;
 #pragma unroll 2
-          for (int i = 0; i < groups; ++i) {
-            // (h, v < half unless the weights change under the call where their keys are read again and again)
-            const uint32_t hb = __ballot_sync(0xffffffffu, hm >> i & 1), mb = __ballot_sync(0xffffffffu, mm >> i & 1);
-            const int hk = h + __popc(hb & lower), vk = v + __popc(mb & lower);
-            if ((hm >> i & 1) && hk < a.half) hole[hk] = r + i * 32;
-            if ((mm >> i & 1) && vk < a.half) move[vk] = r + i * 32;
-            h += __popc(hb);
-            v += __popc(mb);
+          for (int j = 0; j < kPer; ++j) {
+            const uint32_t hb = __ballot_sync(0xffffffffu, hm >> j & 1), mb = __ballot_sync(0xffffffffu, mm >> j & 1);
+            const int at = sm.at[j * kSelWarps + warp], r = r0 + j * kSelThreads + tid;
+            const int h = holes + (at & 0xffff) + __popc(hb & lower), v = movers + (at >> 16) + __popc(mb & lower);
+            // (h, v < half unless the weights change under the call where they are read again and again)
+            if ((hm >> j & 1) && h < a.half) hole[h] = r;
+            if ((mm >> j & 1) && v < a.half) move[v] = r;
           }
+          if (!resident) __syncthreads();  // sm.at is read before the next chunk writes it
         }
         holes += all & 0xffff;
         movers += all >> 16;
       }
       if (pass == 0) {
         if (tid < C) {
-          SelExchange* to = C == 1 ? &sm.from[0] : cl.map_shared_rank(&sm.from[rank], tid);
+          SelExchange* to = peer(&sm.from[C == 1 ? 0 : rank], tid);
           to->holes = holes;
           to->movers = movers;
         }
@@ -554,12 +539,11 @@ __global__ void __launch_bounds__(kSelThreads)
     cnt = min(cnt, (int)a.half);
   }
   // (every access to another CTA's shared memory came before the last barrier that its owner passed)
-  if (all_here || n - m <= kFew) {
+  if constexpr (kWords > 0) {
     sync();  // the lists are written
     constexpr int kRows = 4;
     for (int i = (rank * kSelWarps + warp) * kRows; i < cnt; i += C * kSelWarps * kRows)
       move_rows<kWords, kRows>(a, bh, i, min(kRows, cnt - i), lane);
-    cnt = 0;
   }
   if (rank == 0 && tid == 0) {
     a.count[bh] = cnt;
@@ -678,17 +662,19 @@ cudaError_t launch_kv_evict(const Plan& p, const KvView& c, const int32_t* budge
   while (a.cluster < kMaxCluster && (int64_t)a.BH * a.cluster * 2 <= kNumSMs && a.cluster * 2 * 1024 <= c.max_len)
     a.cluster *= 2;
   const int run = (int)ceil_div64(c.max_len, a.cluster);
-  const int cached = run <= kSelCached;
-  const size_t smem = cached ? (size_t)run * 8 : 0;
-  const int all_here = run <= 2048;
   const int words = p.cfg.d_h * p.esize / 8;
-  auto select = words == 16 ? kv_select_kernel<16> : words == 32 ? kv_select_kernel<32> : kv_select_kernel<64>;
-  static std::atomic<uint64_t> ready[3];
-  cudaError_t e = allow_smem((const void*)select, kSelCached * 8, ready[words == 16 ? 0 : words == 32 ? 1 : 2]);
-  if (e != cudaSuccess) return e;
+  // At most half the rows move.  With 2048 rows per CTA the clusters make the moves in no more time than the second
+  // kernel does, launch included (us replayed, here / second kernel: 64 pairs of 4096 rows, half of them dropped 35 /
+  // 38, 96 dropped 18 / 25; 8 pairs 20 / 20 and 16 / 20), and the host saves a launch.
+  const bool all_here = run <= kPerSmall * kSelThreads;
+  auto select = !all_here     ? kv_select_kernel<kPerLarge, 0>
+                : words == 16 ? kv_select_kernel<kPerSmall, 16>
+                : words == 32 ? kv_select_kernel<kPerSmall, 32>
+                              : kv_select_kernel<kPerSmall, 64>;
+  cudaError_t e;
   {
     ProfScope ps(p, st, KID_KV_SELECT);
-    e = launch_pdl_cluster(select, (unsigned)(a.BH * a.cluster), kSelThreads, a.cluster, smem, st, a, cached, all_here);
+    e = launch_pdl_cluster(select, (unsigned)(a.BH * a.cluster), kSelThreads, a.cluster, 0, st, a);
   }
   if (e != cudaSuccess || all_here) return e;
   auto move = words == 16 ? kv_move_kernel<16> : words == 32 ? kv_move_kernel<32> : kv_move_kernel<64>;

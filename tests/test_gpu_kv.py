@@ -398,6 +398,8 @@ EVICT = [
     ("half", KvCase([[1000, 999], [3, 2500]], 2), 2, 2, 10),
     ("guard_only", KvCase([[500, 20]], 2, page=32), 8, 5, 30),
     ("long", KvCase([[20000, 30011]], 2, d=64, page=128), 5, 4, 100),
+    # a CTA per pair, whose rows do not fit its registers
+    ("chunks", KvCase([[17 + i, 17003 if i == 5 else 40] for i in range(19)] * 2 + [[33000, 1]], 2, d=64, page=256), 3, 4, 50),
     ("f32", KvCase([[300, 700, 0]], 3, dtype=dkv.F32), 2, 1, 0),
     ("f32_d64", KvCase([[1, 2, 130]], 3, d=64, page=16, dtype=dkv.F32), 2, 0, 0),
 ]
