@@ -500,20 +500,28 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
           }
 #pragma unroll 2
           for (int j = 0; j < kPer; ++j) {
-            const uint32_t hb = __ballot_sync(0xffffffffu, hm >> j & 1), mb = __ballot_sync(0xffffffffu, mm >> j & 1);
-            if (lane == 0) sm.at[j * kSelWarps + warp] = __popc(hb) | __popc(mb) << 16;
+            const int g0 = r0 + j * kSelThreads;  // (holes lie below m, movers at or past it)
+            const int holes_j = g0 < m ? __popc(__ballot_sync(0xffffffffu, hm >> j & 1)) : 0;
+            const int movers_j = g0 + kSelThreads > m ? __popc(__ballot_sync(0xffffffffu, mm >> j & 1)) : 0;
+            if (lane == 0) sm.at[j * kSelWarps + warp] = holes_j | movers_j << 16;
           }
           all = scan_counts<kPer * kSelWarps>(sm);
         }
         if (pass == 1) {
 #pragma unroll 2
           for (int j = 0; j < kPer; ++j) {
-            const uint32_t hb = __ballot_sync(0xffffffffu, hm >> j & 1), mb = __ballot_sync(0xffffffffu, mm >> j & 1);
-            const int at = sm.at[j * kSelWarps + warp], r = r0 + j * kSelThreads + tid;
-            const int h = holes + (at & 0xffff) + __popc(hb & lower), v = movers + (at >> 16) + __popc(mb & lower);
+            const int at = sm.at[j * kSelWarps + warp], g0 = r0 + j * kSelThreads;
             // (h, v < half unless the weights change under the call where they are read again and again)
-            if ((hm >> j & 1) && h < a.half) hole[h] = r;
-            if ((mm >> j & 1) && v < a.half) move[v] = r;
+            if (g0 < m) {
+              const uint32_t b = __ballot_sync(0xffffffffu, hm >> j & 1);
+              const int h = holes + (at & 0xffff) + __popc(b & lower);
+              if ((hm >> j & 1) && h < a.half) hole[h] = g0 + tid;
+            }
+            if (g0 + kSelThreads > m) {
+              const uint32_t b = __ballot_sync(0xffffffffu, mm >> j & 1);
+              const int v = movers + (at >> 16) + __popc(b & lower);
+              if ((mm >> j & 1) && v < a.half) move[v] = g0 + tid;
+            }
           }
           if (!resident) __syncthreads();  // sm.at is read before the next chunk writes it
         }
