@@ -251,12 +251,18 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
   uint32_t key[kPer];
   int ps[kPer];
   auto load = [&](int r0) {
+    const float* wp = w + r0 + tid;
+    const int32_t* pp = pos + r0 + tid;
+    const int in = hi - r0 - tid;  // the j-th row is there where j kSelThreads < in
     float wv[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const int r = r0 + j * kSelThreads + tid;
-      wv[j] = r < hi ? __ldcg(w + r) : 0.f;
-      ps[j] = r < hi ? __ldcg(pos + r) : 0;
+      wv[j] = 0.f;
+      ps[j] = 0;
+      if (j * kSelThreads < in) {
+        wv[j] = __ldcg(wp + j * kSelThreads);
+        ps[j] = __ldcg(pp + j * kSelThreads);
+      }
     }
 #pragma unroll
     for (int j = 0; j < kPer; ++j) key[j] = weight_key(wv[j]);
@@ -265,9 +271,10 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
   int last = INT32_MIN, bad = 0;
   for (int r0 = lo; r0 < hi; r0 += kChunk) {
     load(r0);
+    const int in = hi - r0 - tid;
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
-      if (r0 + j * kSelThreads + tid < hi) {
+      if (j * kSelThreads < in) {
         kmin = min(kmin, key[j]);
         kmax = max(kmax, key[j]);
         last = max(last, ps[j]);
@@ -317,13 +324,13 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
     }
   }
   int cnt = 0;
-  const int64_t from = (int64_t)last - a.n_recent;
   const bool guards = a.n_first + a.n_recent > 0;
   auto mark = [&] {
-    if (guards)
+    if (guards) {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (ps[j] < a.n_first || ps[j] > from) key[j] = kGuarded;
+      for (int j = 0; j < kPer; ++j)  // (positions are at most `last`; the difference fits 32 bits)
+        if (ps[j] < a.n_first || (uint32_t)last - (uint32_t)ps[j] < (uint32_t)a.n_recent) key[j] = kGuarded;
+    }
   };
   // the keys of a chunk, guarded rows marked
   auto fetch = [&](int r0) {
@@ -401,24 +408,27 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
       __syncthreads();
       for (int r0 = lo; r0 < hi; r0 += kChunk) {
         fetch(r0);
+        const int in = hi - r0 - tid;
+        int guarded = 0;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-          if (r0 + j * kSelThreads >= hi) break;
-          const uint32_t k = key[j], d = k - base;
-          int bin = -1;
-          if (r0 + j * kSelThreads + tid < hi) {
-            if (k == kGuarded)
-              bin = first ? kBins : -1;
-            else if (k >= base && d <= span)
-              bin = (int)(d >> shift);
+          // (a key below base wraps round to far above span, and no range reaches the guarded rows' key)
+          const uint32_t d = key[j] - base;
+          const bool is = j * kSelThreads < in && d <= span;
+          if (first) guarded += j * kSelThreads < in && key[j] == kGuarded;
+          if (__any_sync(0xffffffffu, is)) {
+            // rows of equal weight would queue up at one counter
+            const uint32_t bin = d >> shift, bin0 = __shfl_sync(0xffffffffu, bin, 0);
+            if (__all_sync(0xffffffffu, is && bin == bin0)) {
+              if (lane == 0) atomicAdd(&hist[bin], 32);
+            } else if (is) {
+              atomicAdd(&hist[bin], 1);
+            }
           }
-          if (!__any_sync(0xffffffffu, bin >= 0)) continue;
-          // rows of equal weight would queue up at one counter
-          if (__all_sync(0xffffffffu, bin == __shfl_sync(0xffffffffu, bin, 0))) {
-            if (lane == 0) atomicAdd(&hist[bin], 32);
-          } else if (bin >= 0) {
-            atomicAdd(&hist[bin], 1);
-          }
+        }
+        if (first && guards) {
+          guarded = __reduce_add_sync(0xffffffffu, guarded);
+          if (lane == 0 && guarded) atomicAdd(&hist[kBins], guarded);
         }
       }
       sync();
@@ -468,17 +478,24 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
         int all = 0;
         if (pass == 0 || !resident) {  // (of a single chunk, the first pass has it all)
           fetch(r0);
-          uint32_t eq = 0;
+          const int in = hi - r0 - tid, low = m - r0 - tid;  // the j-th row is there; is below m
+          const uint32_t least = ties ? base + 1 : base;      // (ties among the guarded rows: none is above them)
+          const bool none = ties && base == kGuarded;
           hm = mm = 0;
 #pragma unroll
           for (int j = 0; j < kPer; ++j) {
-            const int r = r0 + j * kSelThreads + tid;
-            const bool in = r < hi, keep = key[j] > base || (!ties && key[j] == base);
-            hm |= (uint32_t)(in && r < m && !keep) << j;
-            mm |= (uint32_t)(in && r >= m && keep) << j;
-            eq |= (uint32_t)(in && key[j] == base) << j;
+            const bool keep = !none && key[j] >= least;
+            if (j * kSelThreads < in) {
+              if (j * kSelThreads < low)
+                hm |= keep ? 0u : 1u << j;
+              else
+                mm |= keep ? 1u << j : 0u;
+            }
           }
           if (ties) {
+            uint32_t eq = 0;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) eq |= (uint32_t)(j * kSelThreads < in && key[j] == base) << j;
 #pragma unroll 2
             for (int j = 0; j < kPer; ++j) {
               const uint32_t b = __ballot_sync(0xffffffffu, eq >> j & 1);
@@ -489,7 +506,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
             for (int j = 0; j < kPer; ++j) {
               const uint32_t b = __ballot_sync(0xffffffffu, eq >> j & 1);
               if ((eq >> j & 1) && eq_at + sm.at[j * kSelWarps + warp] + __popc(b & lower) < need) {  // kept after all
-                if (r0 + j * kSelThreads + tid < m)
+                if (j * kSelThreads < low)
                   hm &= ~(1u << j);
                 else
                   mm |= 1u << j;
