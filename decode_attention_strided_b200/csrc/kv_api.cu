@@ -114,6 +114,7 @@ deltakv_status deltakv_kv_append(deltakv_plan_t plan, const deltakv_kv_cache* ca
   if (st != DELTAKV_OK) return st;
   if (!K || !V || !kv_strides || (pos && !first_pos)) return DELTAKV_ERR_INVALID_ARG;
   if ((weights || pos) && cap < cache->max_len) return DELTAKV_ERR_INVALID_ARG;
+  if ((int64_t)p.cfg.batch * p.cfg.kv_heads * ceil_div64(n_new, 64) > INT32_MAX) return DELTAKV_ERR_UNSUPPORTED;
   if (workspace_bytes < kErrBytes) return DELTAKV_ERR_WORKSPACE;
   for (int i = 0; i < 3; ++i)
     if (kv_strides[i] < 0 || (kv_strides[i] * p.esize) % 16 != 0) return DELTAKV_ERR_ALIGNMENT;

@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
     if (guards) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j)  // (positions are at most `last`; the difference fits 32 bits)
-        if (ps[j] < a.n_first || (uint32_t)last - (uint32_t)ps[j] < (uint32_t)a.n_recent) key[j] = kGuarded;
+        if ((uint32_t)ps[j] < (uint32_t)a.n_first || (uint32_t)last - (uint32_t)ps[j] < (uint32_t)a.n_recent) key[j] = kGuarded;
     }
   };
   // the keys of a chunk, guarded rows marked

@@ -417,6 +417,8 @@ def _kv_meta(name, t, dtype, pairs, dev):
     if not isinstance(t, torch.Tensor) or t.dim() != 3:
         raise ValueError(f"{name} must be a tensor {list(pairs) + ['cap']}")
     cap = t.shape[2]
+    if cap > 0x7fffffff:
+        raise ValueError(f"{name}: cap does not fit 32 bits")
     return _kv_tensor(name, t, dtype, (*pairs, cap), dev), cap
 
 
@@ -453,9 +455,11 @@ class KVCache:
         self.plan, self.pool, self.page_table, self.lens = p, pool, page_table, lens
         self._fields = (pp, n_pages, page, tp, max_pages, lp)
 
-    def _call(self, p, max_len, workspace, stream):
+    def _call(self, fn, p, max_len, workspace, stream):
         """What every kv call passes: the C view, the workspace, its bytes and
         the stream."""
+        if not 0 < max_len <= p.cfg.max_T:  # (ctypes would wrap it round)
+            raise DeltaKVError(fn, 1)
         if self.plan is not p and self.plan.cfg != p.cfg:
             raise ValueError("the cache belongs to a plan of another configuration")
         if self.dev < 0 or self.dev != torch.cuda.current_device():
@@ -493,7 +497,7 @@ def kv_append(p: Plan, cache: KVCache, max_len: int, K, V, workspace, n_tokens=N
     pp, cap_p = (None, cap) if pos is None else _kv_meta("pos", pos, torch.int32, (B, H), dev)
     if w is not None and cap != cap_p:
         raise ValueError(f"weights and pos must have the same cap, got {cap} and {cap_p}")
-    view, ws, nbytes, st = cache._call(p, max_len, workspace, stream)
+    view, ws, nbytes, st = cache._call("deltakv_kv_append", p, max_len, workspace, stream)
     code = _lib.deltakv_kv_append(p.handle, view, n_new, K.data_ptr(), V.data_ptr(),
                                   _I3(ks[0] if B > 1 else 0, ks[1] if H > 1 else 0, ks[2] if n_new > 1 else d), nt, fp,
                                   w, pp, cap_p, tw, ws, nbytes, st)
@@ -512,7 +516,7 @@ def kv_decode_attention(p: Plan, cache: KVCache, max_len: int, q, out, workspace
     os_ = _kv_rows("out", out, torch.float32, shape, dev)
     w, cap = (None, 0) if weights is None else _kv_meta("weights", weights, torch.float32, (c.batch, c.kv_heads), dev)
     lp = None if lse is None else _kv_tensor("lse", lse, torch.float32, shape[:2], dev)
-    view, ws, nbytes, st = cache._call(p, max_len, workspace, stream)
+    view, ws, nbytes, st = cache._call("deltakv_kv_decode_attention", p, max_len, workspace, stream)
     many, heads = c.batch > 1, c.q_heads > 1
     code = _lib.deltakv_kv_decode_attention(
         p.handle, view, q.data_ptr(), _I2(qs[0] if many else 0, qs[1] if heads else 0), out.data_ptr(),
@@ -528,6 +532,8 @@ def kv_evict(p: Plan, cache: KVCache, max_len: int, budget, weights, pos, worksp
     the largest weights.  lens_out, weights_out and pos_out default to
     cache.lens, weights and pos (in place)."""
     dev = cache.dev
+    if n_first < 0 or n_recent < 0 or n_first + n_recent > p.cfg.max_T:  # (ctypes would wrap them round)
+        raise DeltaKVError("deltakv_kv_evict", 1)
     pairs = (p.cfg.batch, p.cfg.kv_heads)
     w, cap = _kv_meta("weights", weights, torch.float32, pairs, dev)
     shape = (*pairs, cap)
@@ -536,7 +542,7 @@ def kv_evict(p: Plan, cache: KVCache, max_len: int, budget, weights, pos, worksp
     po = pp if pos_out is None else _kv_tensor("pos_out", pos_out, torch.int32, shape, dev)
     bp = _kv_tensor("budget", budget, torch.int32, pairs, dev)
     lo = _kv_tensor("lens_out", cache.lens if lens_out is None else lens_out, torch.int32, pairs, dev)
-    view, ws, nbytes, st = cache._call(p, max_len, workspace, stream)
+    view, ws, nbytes, st = cache._call("deltakv_kv_evict", p, max_len, workspace, stream)
     code = _lib.deltakv_kv_evict(p.handle, view, bp, n_first, n_recent, w, pp, wo, po, cap, lo, ws, nbytes, st)
     if code:
         _check("deltakv_kv_evict", code)

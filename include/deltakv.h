@@ -364,7 +364,8 @@ typedef struct {
  * [0, n_pages) is never followed (its rows are skipped) and a length outside
  * [0, max_len] is read as 0; both are reported as DELTAKV_ERR_DEVICE_BOUNDS.
  * Entries of page_table past a pair's last page are not read.  Calls that
- * write rows need each of a table's pages to be its only holder's. */
+ * write rows (append, evict) need each of the pages to be in the table once.
+ * UNSUPPORTED: B H ceil(max_len / 16) of 2^31 and more. */
 typedef struct {
     void* pool;                 /* device, 16-byte aligned, pool_bytes */
     int32_t n_pages;
@@ -401,8 +402,8 @@ deltakv_status deltakv_kv_pool_layout(deltakv_plan_t plan, int32_t n_pages, int3
  *                token got before it came here, as from a prefill)
  *   cap        : row stride of weights and pos, >= max_len (ignored if both
  *                are NULL)
- *   workspace  : deltakv_kv_layout.workspace_bytes (its error word only).
- * Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, CUDA. */
+ *   workspace  : at least 256 bytes (its error word only).
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, WORKSPACE, CUDA. */
 deltakv_status deltakv_kv_append(deltakv_plan_t plan, const deltakv_kv_cache* cache, int32_t n_new,
                                  const void* K, const void* V, const int64_t kv_strides[3],
                                  const int32_t* n_tokens, const int32_t* first_pos, float* weights,
@@ -423,7 +424,9 @@ deltakv_status deltakv_kv_append(deltakv_plan_t plan, const deltakv_kv_cache* ca
  *   decay      : >= 0 and finite (1: plain sums); ignored without weights
  *   workspace  : workspace_bytes, or weights_workspace_bytes with weights, of
  *                the layout for this max_len; scratch.
- * Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, CUDA. */
+ * A NaN or an infinity in a valid row has the effect that the formulas give
+ * it, in its pair alone; rows that are not valid are never used, whatever they
+ * hold.  Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, WORKSPACE, CUDA. */
 deltakv_status deltakv_kv_decode_attention(deltakv_plan_t plan, const deltakv_kv_cache* cache, const void* q,
                                            const int64_t q_strides[2], float* out, const int64_t out_strides[2],
                                            float* lse, float* weights, int32_t cap, float decay, void* workspace,
@@ -431,8 +434,9 @@ deltakv_status deltakv_kv_decode_attention(deltakv_plan_t plan, const deltakv_kv
 
 /* Drop the rows with the least accumulated attention weight.  Of the n rows
  * of a (sequence, kv-head), m = min(n, max(budget[b][h], n_first + n_recent))
- * are kept: those whose position is below n_first or among the last n_recent
- * positions (pos > max pos - n_recent), then those with the largest weights
+ * are kept: those whose position is one of the first n_first (0 <= pos <
+ * n_first) or of the last n_recent (pos > max pos - n_recent), then those with
+ * the largest weights
  * (NaN ranks lowest; ties to the lower row).  Kept rows below m stay where
  * they are; kept rows at or past m move, in order, into the dropped rows below
  * m, so that rows 0 .. m-1 are the kept ones and only what has to move moves
@@ -448,7 +452,8 @@ deltakv_status deltakv_kv_decode_attention(deltakv_plan_t plan, const deltakv_kv
  *   lens_out   : device int32 [B][H], set to m; may be cache->lens
  *   workspace  : workspace_bytes of the layout for this max_len.
  * A pair with a page index out of range among its first n rows is left whole
- * (m = n) and reported.  Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, CUDA. */
+ * (m = n) and reported.  Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT,
+ * WORKSPACE, CUDA. */
 deltakv_status deltakv_kv_evict(deltakv_plan_t plan, const deltakv_kv_cache* cache, const int32_t* budget,
                                 int32_t n_first, int32_t n_recent, const float* weights, const int32_t* pos,
                                 float* weights_out, int32_t* pos_out, int32_t cap, int32_t* lens_out,

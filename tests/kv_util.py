@@ -129,8 +129,9 @@ def evict64(n, budget, n_first, n_recent, w, pos):
     if m == n:
         return m, np.arange(n)
     pos = pos.astype(np.int64)
-    guarded = (pos < n_first) | (pos > pos.max() - n_recent)
-    w = w.astype(np.float64)
+    guarded = ((pos >= 0) & (pos < n_first)) | (pos > pos.max() - n_recent)
+    with np.errstate(invalid="ignore"):  # signalling NaN
+        w = w.astype(np.float64)
     # ascending sort of (class, -weight, row): guarded, then numbers by weight, then NaN
     cls = np.where(guarded, 0, np.where(np.isnan(w), 2, 1))
     neg = np.where(cls == 1, -np.nan_to_num(w, nan=0.0, posinf=np.inf, neginf=-np.inf), 0.0)

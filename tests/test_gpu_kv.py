@@ -1,5 +1,7 @@
 """Plain paged cache on the GPU: append, decode attention and eviction against
 plain implementations in 64 bits (kv_util)."""
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
@@ -78,6 +80,8 @@ ATTEND = [
     ("long", KvCase([[20011, 5]], 8)),
     ("many_pairs", KvCase([[(37 * i + 11 * h) % 300 for h in range(8)] for i in range(40)], 32)),
     ("peaked", KvCase([[3001, 900]], 8, scale=6.0)),
+    ("mostly_empty", KvCase([[300 if h in (3, 290, 580, 599) else 0 for h in range(600)]], 600, d=64, page=32)),
+    ("full_clusters", KvCase([[500, 33, 90, 1, 0, 256, 255, 511]] * 4, 32, page=32)),
     ("f32", KvCase([[1000, 3], [64, 129]], 16, dtype=dkv.F32)),
     ("f32_d64_g1", KvCase([[2049, 16, 0]], 3, d=64, page=16, dtype=dkv.F32)),
     ("f32_g3", KvCase([[5003, 100]], 6, page=32, dtype=dkv.F32, scale=3.0)),
@@ -87,7 +91,14 @@ ATTEND = [
 
 @pytest.mark.parametrize("name,case", ATTEND, ids=[n for n, _ in ATTEND])
 @pytest.mark.parametrize("weights", [False, True], ids=["plain", "weights"])
-def test_attend(name, case, weights):
+@pytest.mark.parametrize("form", ["as_is", "cut"])
+def test_attend(name, case, weights, form):
+    """Short rows take a cluster per pair; a bound far above the lengths
+    (form "cut") makes the same rows go through the cut over the whole GPU."""
+    if form == "cut":
+        if case.B * case.H > 32:
+            pytest.skip("goes through the cut as it is")
+        case = dataclasses.replace(case, max_len=40000)
     s = Setup(case)
     decay = 0.75 if case.seed == 0 and case.G % 2 else 1.0
     out, lse, w = _attend(s, weights, decay)
@@ -95,8 +106,9 @@ def test_attend(name, case, weights):
     _check_attend(s, out, lse, w, decay)
 
 
-def test_attend_is_deterministic_and_optional_outputs_change_nothing():
-    s = Setup(KvCase([[9001, 40], [300, 2000]], 8))
+@pytest.mark.parametrize("longest", [9001, 901], ids=["cut", "cluster"])
+def test_attend_is_deterministic_and_optional_outputs_change_nothing(longest):
+    s = Setup(KvCase([[longest, 40], [300, 700]], 8))
     first = _attend(s)
     for _ in range(3):
         again = _attend(s)
@@ -127,8 +139,10 @@ def test_attend_strided_queries_and_outputs():
     assert (buf[:, :, c.d:] == 7.0).all()
 
 
-def test_attend_infinities_and_nan_in_valid_rows_stay_in_their_pair():
-    c = KvCase([[100, 100], [90, 30]], 4)
+@pytest.mark.parametrize("max_len", [0, 40000], ids=["cluster", "cut"])
+@pytest.mark.parametrize("Hq,dtype", [(4, dkv.BF16), (8, dkv.BF16), (16, dkv.BF16), (4, dkv.F32)])
+def test_attend_infinities_and_nan_in_valid_rows_stay_in_their_pair(max_len, Hq, dtype):
+    c = KvCase([[100, 100], [90, 30]], Hq, max_len=max_len, dtype=dtype)
     s = Setup(c)
     ids = s.table_host
     s.pool[0, ids[0, 0, 1], 3, 5] = float("nan")
@@ -136,14 +150,18 @@ def test_attend_infinities_and_nan_in_valid_rows_stay_in_their_pair():
     out, lse, w = _attend(s)
     assert dkv.device_status(s.p, s.ws) == 0
     _check_attend(s, out, lse, w, pairs=[(0, 1), (1, 0)])
-    assert torch.isnan(out[0, :2]).all()
-    got = out[1, 2:4]
+    G = Hq // 2
+    assert torch.isnan(out[0, :G]).all()
+    got = out[1, G:]
     assert torch.isinf(got[:, 7]).all() and torch.isfinite(got[:, :7]).all() and torch.isfinite(got[:, 8:]).all()
 
 
-def test_attend_bad_page_is_skipped_and_reported():
-    c = KvCase([[300, 200], [300, 64]], 8)
+@pytest.mark.parametrize("max_len,page", [(300, 64), (40000, 64), (40000, 16), (300, 16)])
+def test_attend_bad_page_is_skipped_and_reported(max_len, page):
+    c = KvCase([[300, 200], [300, 64]], 8, max_len=max_len, page=page)
     s = Setup(c)
+    first, last = (64, 128) if page == 64 else (16, 32)  # the rows that are lost
+    gone = last - first
     for bad in (-1, s.pool.shape[1]):
         t = s.table_host.clone()
         t[0, 0, 1] = bad
@@ -151,24 +169,27 @@ def test_attend_bad_page_is_skipped_and_reported():
         out, lse, w = _attend(s)
         assert dkv.device_status(s.p, s.ws) == BOUNDS
         assert dkv.device_status(s.p, s.ws) == 0
-        K, V = s.K[0, 0], s.V[0, 0]
-        s.K[0, 0] = torch.cat([K[:64], K[128:]])
-        s.V[0, 0] = torch.cat([V[:64], V[128:]])
-        saved, s.w = s.w, s.w.clone()
-        c.lens[0][0] = 236
         # the skipped rows get no weight; the check below has the others in order
+        assert torch.equal(w[0, 0, first:last].cpu(), s.w[0, 0, first:last])
+        r = Setup.__new__(Setup)
+        r.__dict__.update(s.__dict__)
+        r.c = dataclasses.replace(c, lens=[[300 - gone, 200], [300, 64]], max_len=c.n)
+
+        def without(x):
+            return torch.cat([x[:first], x[last:300]])
+
+        r.K, r.V, r.w = dict(s.K), dict(s.V), s.w.clone()
+        r.K[0, 0], r.V[0, 0] = without(s.K[0, 0]), without(s.V[0, 0])
+        r.w[0, 0, :300 - gone] = without(s.w[0, 0])
         wr = w.clone()
-        assert torch.equal(wr[0, 0, 64:128].cpu(), saved[0, 0, 64:128])
-        wr[0, 0, :236] = torch.cat([w[0, 0, :64], w[0, 0, 128:300]])
-        wr[0, 0, 236:] = saved[0, 0, 236:].cuda()
-        s.w[0, 0, :236] = torch.cat([saved[0, 0, :64], saved[0, 0, 128:300]])
-        _check_attend(s, out, lse, wr)
-        s.w, c.lens[0][0] = saved, 300
-        s.K[0, 0], s.V[0, 0] = K, V
+        wr[0, 0, :300 - gone] = without(w[0, 0])
+        wr[0, 0, 300 - gone:] = r.w[0, 0, 300 - gone:].cuda()
+        _check_attend(r, out, lse, wr)
 
 
-def test_attend_all_pages_bad_gives_an_empty_row():
-    s = Setup(KvCase([[40, 50]], 2))
+@pytest.mark.parametrize("max_len", [0, 40000], ids=["cluster", "cut"])
+def test_attend_all_pages_bad_gives_an_empty_row(max_len):
+    s = Setup(KvCase([[40, 50]], 2, max_len=max_len))
     s.table[0, 0] = -5
     out, lse, w = _attend(s)
     assert dkv.device_status(s.p, s.ws) == BOUNDS
@@ -177,9 +198,10 @@ def test_attend_all_pages_bad_gives_an_empty_row():
     _check_attend(s, out, lse, w, pairs=[(0, 1)])
 
 
-@pytest.mark.parametrize("bad", [-1, 301, 2**31 - 1])
-def test_attend_bad_length_is_an_empty_row_and_reported(bad):
-    c = KvCase([[300, 200], [299, 64]], 8)
+@pytest.mark.parametrize("max_len", [300, 40000], ids=["cluster", "cut"])
+@pytest.mark.parametrize("bad", [-1, 40001, 2**31 - 1])
+def test_attend_bad_length_is_an_empty_row_and_reported(bad, max_len):
+    c = KvCase([[300, 200], [299, 64]], 8, max_len=max_len)
     s = Setup(c)
     s.lens[1, 0] = bad
     out, lse, w = _attend(s)
@@ -435,6 +457,31 @@ def test_evict_bad_pages_and_lengths_leave_the_pair_whole():
     s.lens[0, 2] = 301
     s.c = KvCase([[300, 200, 0]], 3)
     assert _evict_check(s, [[100, 100, 100]], 0, 0, w, pos, False) == BOUNDS
+
+
+def test_evict_one_array_in_place_and_the_other_apart():
+    c = KvCase([[700, 90]], 2)
+    for which in (0, 1):
+        s = Setup(c)
+        w, pos = _meta(c, 4, "random")
+        wd, pd = w.cuda(), pos.cuda()
+        wo, po = (wd, torch.zeros_like(pd)) if which else (torch.zeros_like(wd), pd)
+        lo = torch.zeros_like(s.lens)
+        dkv.kv_evict(s.p, s.cache, c.n, torch.tensor([[300, 80]], dtype=torch.int32, device="cuda"), wd, pd, s.ws,
+                     n_first=1, n_recent=20, lens_out=lo, weights_out=wo, pos_out=po)
+        assert dkv.device_status(s.p, s.ws) == 0
+        for h, (n, b) in enumerate(((700, 300), (90, 80))):
+            m, src = evict64(n, b, 1, 20, w[0, h, :n].numpy(), pos[0, h, :n].numpy())
+            assert _same(wo[0, h, :m], w[0, h][src]) and _same(po[0, h, :m], pos[0, h][src]) and int(lo[0, h]) == m
+
+
+def test_evict_negative_positions_are_not_the_first():
+    c = KvCase([[300, 299]], 2)
+    for n_first, n_recent in ((0, 0), (5, 0), (0, 7), (5, 7)):
+        s = Setup(c)
+        w, pos = _meta(c, 4, "random")
+        pos -= 450
+        assert _evict_check(s, [[120, 296]], n_first, n_recent, w, pos, False) == 0
 
 
 def test_evict_repeated_positions_stay_in_bounds():

@@ -197,6 +197,11 @@ def test_binding_refuses_what_the_kernels_would_misread(lib):
         with pytest.raises(ValueError):
             dkv.kv_evict(p, cache, 10, kw.get("bud", bud), kw.get("w", w), kw.get("pos", pos), ws,
                          weights_out=kw.get("wo"), pos_out=kw.get("po"), lens_out=kw.get("lo"))
+    # what does not fit 32 bits is refused, not wrapped round
+    for kw in (dict(max_len=2**32 + 10), dict(max_len=0), dict(n_first=2**32), dict(n_recent=-1)):
+        with pytest.raises((ValueError, dkv.DeltaKVError)) as e:
+            dkv.kv_evict(p, cache, kw.pop("max_len", 10), bud, w, pos, ws, **kw)
+        assert e.type is dkv.DeltaKVError and e.value.code == INVALID
     other = _plan(q_heads=4)
     with pytest.raises(ValueError):
         dkv.kv_evict(other, cache, 10, bud, w, pos, ws)
