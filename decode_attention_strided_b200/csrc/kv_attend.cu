@@ -294,6 +294,7 @@ struct Loader {
   int get = 0, gslot = 0, parity = 0;
   uint32_t good = 0;       // bit k of units issued last in the high bits: group k's rows are there
   bool dead = false;
+  const uint64_t policy = sm100::l2_evict_first();  // a step reads its rows once
 
   __device__ __forceinline__ Loader(const Lens& l_, RingSmem& s_, int w, int l, Place p, int u, int e)
       : lens(l_), sm(s_), warp(w), lane(l), u_end(e), u0(u), at(p) {
@@ -334,12 +335,12 @@ struct Loader {
         sm100::mbar_arrive_expect_tx(bar, total);
       else
         sm100::mbar_arrive(bar);
-      if (one && total) sm100::bulk_load(dst, plane + o, total, bar);
+      if (one && total) sm100::bulk_load_hint(dst, plane + o, total, bar, policy);
     }
     if (!one) {
       __syncwarp();
       if (lane / kGroups == nth && off >= 0)
-        sm100::bulk_load(dst + lane % kGroups * kGroup * kRowBytes, plane + o, rows * kRowBytes, bar);
+        sm100::bulk_load_hint(dst + lane % kGroups * kGroup * kRowBytes, plane + o, rows * kRowBytes, bar, policy);
     }
     ++put;
     if (++slot == kSlots) slot = 0;
