@@ -31,7 +31,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kGroup = 16;         // rows of the smallest page
 constexpr int kSlotBytes = 8192;   // K or V rows of one unit of the split
-constexpr int kSlots = 3;          // of a warp's ring
+constexpr int kSlots = 2;          // of a warp's ring: K rows, V rows
 constexpr int kMinUnits = 4;       // a CTA gets at least these, or fewer CTAs work
 // A cluster per pair instead of the cut (one kernel instead of two): where its
 // CTAs find room at once (16 clusters of eight did not, 32 of four did) and take
@@ -174,7 +174,7 @@ struct Lens {
 // the block meets once for all of them.
 template <int DH, int GP>
 struct Merge {
-  static constexpr int kBufs = GP >= 4 ? 8 / GP : 4;
+  static constexpr int kBufs = GP >= 4 ? 16 / GP : 4;
   float m[kBufs][kWarps][GP], l[kBufs][kWarps][GP];
   float o[kBufs][kWarps][GP][DH];
   int bh[kBufs], slot[kBufs];  // whose part it is; partial slot, or -1 where the segment is the whole pair
@@ -252,16 +252,17 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // ---- the rows' way into shared memory
-// A warp takes every eighth unit of its CTA's range through a ring of three
-// 8 KB slots of its own, K rows and V rows in turn: lane 0 issues bulk copies
-// (one per slot where a page holds a unit, else one per page), a barrier per
-// slot tells when they have landed, and a slot is refilled as soon as its rows
-// are in registers.  No other warp takes part, so the warps drift freely
-// between the segments' ends.  Plain copies in this pattern reach 7.3 TB/s with
-// 8 KB copies and 96 to 128 KB in flight per SM, 6.6 with 4 KB copies and 192
-// KB, 5.3 with 2 KB copies.
+// A warp takes every eighth unit of its CTA's range through a slot for K rows
+// and one for V rows of its own: lane 0 issues bulk copies (one per slot where
+// a page holds a unit, else one per page), a barrier per slot tells when they
+// have landed, and a slot is refilled as soon as its rows are in registers.  No
+// other warp takes part, so the warps drift freely between the segments' ends.
+// Plain copies in this pattern reach 7.3 TB/s with 8 KB copies and 96 to 128 KB
+// in flight per SM, 6.6 with 4 KB copies and 192 KB, 5.3 with 2 KB copies; a
+// third slot made 64 pairs of 2000 rows 21.1 us instead of 20.2.
 struct RingSmem {
   alignas(128) char ring[kWarps][kSlots][kSlotBytes];
+  float p[kWarps][33][kMaxG];  // float32 rows: the weights of a unit's rows (at most 32), then the rescaling factors
   int lens[kLensTable];
   uint64_t bar[kWarps][kSlots];
   int dead;  // a wait ran out: nothing more is issued or waited for
@@ -665,7 +666,7 @@ struct Bf16Rows {
 // head's query in registers (64 at most: kL is 4 to 16 by the heads); the GP
 // heads' partial sums are reduced over the kL lanes by exchange steps that
 // leave each lane one head.  Outputs: a lane holds four dims of all heads and
-// reads the rows' weights from shared memory (where the unit's K rows were).
+// reads the rows' weights from shared memory.
 // GP: heads rounded up to a power of two.
 template <int DH, int GP_>
 struct F32Rows {
@@ -715,10 +716,10 @@ struct F32Rows {
   // The unit `in` holds next: `valid` rows (at least one); xl: their logits in
   // global memory, or null.
   __device__ __forceinline__ void step(const AttendArgs& a, Loader<float, DH>& in, int valid, float* xl, int lane) {
-    char* ks = in.take();
+    const char* ks = in.take();
     if (!ks) return;
     const uint32_t have = in.groups();
-    float* p_smem = reinterpret_cast<float*>(ks);  // the rows' weights take the place of the K rows, once those are read
+    float* p_smem = &in.sm.p[in.warp][0][0];
     const int head = head_of(lane);
     float x[kPasses];
     float mx = m;
@@ -752,6 +753,8 @@ struct F32Rows {
       }
       x[j] = v[0] * a.scale2;
     }
+    __syncwarp();  // every lane has read its K rows, and the last unit's weights
+    in.issue();
     const bool full = valid == kRows && have == (1u << (kRows / kGroup)) - 1;
     if (!full) {
       // rows that do not count: whatever the slot holds
@@ -776,7 +779,6 @@ struct F32Rows {
     const float f = ex2(m - mu);
     m = mx;
     l *= f;
-    __syncwarp();  // every lane has read its K rows
 #pragma unroll
     for (int j = 0; j < kPasses; ++j) {
       const float p = ex2(x[j] - mu);
@@ -801,9 +803,7 @@ struct F32Rows {
         if (row < valid && (have >> (row / kGroup) & 1)) add_row(vs, p_smem, row, lane);
       }
     }
-    sm100::fence_async_smem();  // the weights were written by this thread, the next rows come by a bulk copy
     __syncwarp();
-    in.issue();
     in.issue();
   }
 
@@ -905,7 +905,7 @@ __device__ __forceinline__ void init_ring(RingSmem& ring, int warp, int lane) {
   if (threadIdx.x == 0) ring.dead = 0;
 }
 
-// One CTA per SM, eight warps with a 24 KB ring each.
+// One CTA per SM, eight warps with a ring each.
 template <int DH, typename Rows>
 __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_constant__ AttendArgs a) {
   using E = typename Rows::E;
