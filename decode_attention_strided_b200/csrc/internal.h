@@ -251,8 +251,8 @@ constexpr int kKvMaxGrid = kNumSMs;  // CTAs of the attention's split (one per S
 __host__ __device__ constexpr int kv_part_floats(int G, int d_h) { return G * d_h + 2 * kMaxG; }
 struct KvWorkspace {
   size_t part;    // attention: [kKvMaxGrid][2] partial results of kv_part_floats
-  size_t lse2;    // attention with weights: [B H][G] float32 log-sum-exp in units of log2
-  size_t logits;  // attention with weights: [B H][max_len][G] float32, in units of log2
+  size_t norm;    // attention with weights: [B H][G] float32 pairs (m, 1 / l)
+  size_t dots;    // attention with weights: q . K_r, [B H][max_len][G] float32
   size_t attend_end, weights_end;
   size_t count, hole, move;  // eviction: [B H] moves, their target and source rows [B H][max_len / 2]
   size_t evict_end;

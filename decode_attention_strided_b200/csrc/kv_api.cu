@@ -16,10 +16,10 @@ KvWorkspace kv_workspace(const Plan& p, int max_len) {
   size_t off = kErrBytes;
   w.part = off;
   off = align256(off + (size_t)kKvMaxGrid * 2 * kv_part_floats(p.G, c.d_h) * 4);
-  w.lse2 = off;
-  off = align256(off + (size_t)(BH * p.G) * 4);
+  w.norm = off;
+  off = align256(off + (size_t)(BH * p.G) * 8);
   w.attend_end = off;
-  w.logits = off;
+  w.dots = off;
   w.weights_end = align256(off + (size_t)(BH * max_len * p.G) * 4);
   off = kErrBytes;
   w.count = off;

@@ -1,12 +1,15 @@
 // kv_attend.cu -- attention of one new token per sequence over plain K/V rows
 // in pages, split over the rows and joined.
 //
-// For query head hq of pair bh = (sequence, kv-head), with x_r = log2(e) q .
-// K_r / sqrt(d_h) over the pair's valid rows r:
-//   m = max_r x_r,  l = sum_r 2^(x_r - m),  out = (sum_r 2^(x_r - m) V_r) / l,
-//   lse = ln2 (m + log2 l),   and with weights   w_r <- decay w_r + sum_heads 2^(x_r - m) / l.
-// A part of the rows gives (m, l, o = sum 2^(x_r - m) V_r); parts join by
-// m = max m_i, l = sum 2^(m_i - m) l_i, o = sum 2^(m_i - m) o_i.
+// For query head hq of pair bh = (sequence, kv-head), with d_r = q . K_r over
+// the pair's valid rows r and c = log2(e) / sqrt(d_h):
+//   m = c max_r d_r,  l = sum_r 2^(c d_r - m),  out = (sum_r 2^(c d_r - m) V_r) / l,
+//   lse = ln2 (m + log2 l),   and with weights   w_r <- decay w_r + sum_heads 2^(c d_r - m) / l.
+// A part of the rows gives (m, l, o = sum 2^(c d_r - m) V_r); parts join by
+// m = max m_i, l = sum 2^(m_i - m) l_i, o = sum 2^(m_i - m) o_i.  The exponent is
+// one fused multiply-add of the dot product and the rounded m: a logit of 30,
+// rounded by itself, would put 2^-19 into its weight, but m's rounding is the
+// same in numerator and denominator.
 //
 // Split: all pairs' rows, in units of 16 to 64 (8 KB of K), form one list that is cut into as
 // many equal ranges as there are CTAs, so that lengths do not matter for the
@@ -60,8 +63,8 @@ struct AttendArgs {
   int64_t cap;
   float decay, scale2;  // scale2 = log2(e) / sqrt(d_h)
   float* part;    // [CTA][2][kv_part_floats]: o[G][d_h], m[kMaxG], l[kMaxG]
-  float* lse2;    // [BH][G]
-  float* logits;  // [BH][max_len][G] or null
+  float2* norm;   // [BH][G]: m and 1 / l, for the weights
+  float* dots;    // [BH][max_len][G]: q . K_r, for the weights
 };
 
 // The cut of the unit list into ranges: the first `rem` of them hold per + 1
@@ -190,7 +193,7 @@ __device__ __forceinline__ void write_out(const AttendArgs& a, int bh, int b, in
       make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
   if (e == 0) {
     const float L = m + log2f(l);
-    if (a.w) a.lse2[(int64_t)bh * a.G + g] = L;
+    if (a.w) a.norm[(int64_t)bh * a.G + g] = make_float2(m, inv);
     if (a.lse) a.lse[(int64_t)bh * a.G + g] = kLn2 * L;
   }
 }
@@ -462,8 +465,8 @@ struct Bf16Rows {
     l[0] = l[1] = 0.f;
   }
 
-  // The unit `in` holds next: `valid` rows (at least one) from row r on; xl:
-  // their logits in global memory, or null.
+  // The unit `in` holds next: `valid` rows (at least one); xl: the place of
+  // their dot products in global memory, or null.
   __device__ __forceinline__ void step(const AttendArgs& a, Loader<E, DH>& in, int valid, float* xl, int lane) {
     const int gr = lane >> 2, t = lane & 3;
     const char* ks = in.take();
@@ -481,7 +484,7 @@ struct Bf16Rows {
         mma_bf16(x1, ka.z, kb.z, ka.w, kb.w, q[i][2], q[i][3]);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[n][i] = (x0[i] + x1[i]) * a.scale2;
+      for (int i = 0; i < 4; ++i) x[n][i] = x0[i] + x1[i];
     }
     __syncwarp();
     in.issue();
@@ -514,20 +517,21 @@ struct Bf16Rows {
     float f[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      float mx = m[c];
+      float mx = -INFINITY;
 #pragma unroll
       for (int n = 0; n < kG; ++n) mx = fmaxf(mx, fmaxf(x[n][c], x[n][c + 2]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+      mx = fmaxf(m[c], mx * a.scale2);
       const float mu = mx == -INFINITY ? 0.f : mx;
       f[c] = ex2(m[c] - mu);
       m[c] = mx;
       l[c] *= f[c];
 #pragma unroll
       for (int n = 0; n < kG; ++n) {
-        x[n][c] = ex2(x[n][c] - mu);
-        x[n][c + 2] = ex2(x[n][c + 2] - mu);
+        x[n][c] = ex2(fmaf(x[n][c], a.scale2, -mu));
+        x[n][c + 2] = ex2(fmaf(x[n][c + 2], a.scale2, -mu));
         l[c] += x[n][c] + x[n][c + 2];
       }
     }
@@ -713,8 +717,8 @@ struct F32Rows {
     l = 0.f;
   }
 
-  // The unit `in` holds next: `valid` rows (at least one); xl: their logits in
-  // global memory, or null.
+  // The unit `in` holds next: `valid` rows (at least one); xl: the place of
+  // their dot products in global memory, or null.
   __device__ __forceinline__ void step(const AttendArgs& a, Loader<float, DH>& in, int valid, float* xl, int lane) {
     const char* ks = in.take();
     if (!ks) return;
@@ -722,7 +726,7 @@ struct F32Rows {
     float* p_smem = &in.sm.p[in.warp][0][0];
     const int head = head_of(lane);
     float x[kPasses];
-    float mx = m;
+    float mx = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kPasses; ++j) {
       const int row = j * kPer + lane / kL;
@@ -751,7 +755,7 @@ struct F32Rows {
           v[0] += __shfl_xor_sync(0xffffffffu, v[0], s);
         }
       }
-      x[j] = v[0] * a.scale2;
+      x[j] = v[0];
     }
     __syncwarp();  // every lane has read its K rows, and the last unit's weights
     in.issue();
@@ -775,13 +779,14 @@ struct F32Rows {
     for (int j = 0; j < kPasses; ++j) mx = fmaxf(mx, x[j]);
 #pragma unroll
     for (int s = kL; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+    mx = fmaxf(m, mx * a.scale2);
     const float mu = mx == -INFINITY ? 0.f : mx;
     const float f = ex2(m - mu);
     m = mx;
     l *= f;
 #pragma unroll
     for (int j = 0; j < kPasses; ++j) {
-      const float p = ex2(x[j] - mu);
+      const float p = ex2(fmaf(x[j], a.scale2, -mu));
       l += p;
       p_smem[(j * kPer + lane / kL) * kMaxG + head] = p;
     }
@@ -881,9 +886,9 @@ __device__ __noinline__ void plain_rows(const AttendArgs& a, Merge<DH, GP>& mg, 
         const auto* vr = reinterpret_cast<const __nv_bfloat16*>(a.c.v) + row * DH;
         float x = 0.f;
         for (int i = 0; i < kN; ++i) x = fmaf(q[i], to_f(kr[i * 32 + lane]), x);
-        x = warp_sum(x) * a.scale2;
-        const float mx = fmaxf(m, x), mu = mx == -INFINITY ? 0.f : mx;
-        const float f = exp2f(m - mu), p = exp2f(x - mu);
+        x = warp_sum(x);
+        const float mx = fmaxf(m, x * a.scale2), mu = mx == -INFINITY ? 0.f : mx;
+        const float f = exp2f(m - mu), p = exp2f(fmaf(x, a.scale2, -mu));
         m = mx;
         l = fmaf(l, f, p);
         for (int i = 0; i < kN; ++i) o[i] = fmaf(o[i], f, p * to_f(vr[i * 32 + lane]));
@@ -944,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
 #pragma unroll 1
     for (; mine < ue; mine += kWarps) {
       const int r = (mine - at.s) * kRows;
-      float* xl = a.w ? a.logits + ((int64_t)at.bh * a.c.max_len + r) * a.G : nullptr;
+      float* xl = a.w ? a.dots + ((int64_t)at.bh * a.c.max_len + r) * a.G : nullptr;
       rows.step(a, in, min(at.len - r, kRows), xl, lane);
     }
     if (!rows.finish(sm.merge, held, warp, lane))
@@ -966,6 +971,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
     }
   }
   in.drain();
+}
+
+// The softmax weight of a row with dot product d (0 where no row of the pair
+// counts for the head).
+__device__ __forceinline__ float weight_of(float d, float2 norm, float scale2) {
+  return norm.x == -INFINITY ? 0.f : exp2f(fmaf(d, scale2, -norm.x)) * norm.y;
 }
 
 // Short rows: a cluster per pair, its CTAs equal runs of the pair's units, the
@@ -999,7 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_short_kernel(const __gr
 #pragma unroll 1
   for (int u = u0 + warp; u < u1; u += kWarps) {
     const int r = u * kRows;
-    float* xl = a.w ? a.logits + ((int64_t)bh * a.c.max_len + r) * a.G : nullptr;
+    float* xl = a.w ? a.dots + ((int64_t)bh * a.c.max_len + r) * a.G : nullptr;
     rows.step(a, in, min(len - r, kRows), xl, lane);
   }
   if (!rows.finish(sm.merge, 0, warp, lane)) plain_rows(a, sm.merge, 0, at, u0 + warp, u1, warp, lane);
@@ -1044,23 +1055,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_short_kernel(const __gr
     write_out<DH>(a, bh, b, h, g, q * 4 % DH, m, l, o);
   }
   if (a.w) {
-    float* L = part + kMaxG * DH + 2 * kMaxG;
+    float2* norm = reinterpret_cast<float2*>(part + kMaxG * DH + 2 * kMaxG);
     if ((int)threadIdx.x < a.G) {
       const int g = threadIdx.x;
       float m = -INFINITY, l = 0.f;
       for (int c = 0; c < C; ++c) m = fmaxf(m, peer(c)[kMaxG * DH + g]);
       const float mu = m == -INFINITY ? 0.f : m;
       for (int c = 0; c < C; ++c) l = fmaf(exp2f(peer(c)[kMaxG * DH + g] - mu), peer(c)[kMaxG * DH + kMaxG + g], l);
-      L[g] = m + log2f(l);
+      norm[g] = make_float2(m, 1.f / l);
     }
     __syncthreads();
     for (int r = u0 * kRows + threadIdx.x; r < min(len, u1 * kRows); r += kThreads) {
-      const float* x = a.logits + ((int64_t)bh * a.c.max_len + r) * a.G;
+      const float* x = a.dots + ((int64_t)bh * a.c.max_len + r) * a.G;
       float* w = a.w + bh * a.cap + r;
       const float old = *w;
       float p = 0.f;
-      for (int g = 0; g < a.G; ++g)
-        if (L[g] != -INFINITY) p += exp2f(__ldcg(x + g) - L[g]);
+      for (int g = 0; g < a.G; ++g) p += weight_of(__ldcg(x + g), norm[g], a.scale2);
       *w = fmaf(a.decay, old, p);
     }
   }
@@ -1140,12 +1150,12 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(const __grid_constant
   }
 }
 
-// w_r <- decay w_r + sum over heads of 2^(x_r - L): a CTA takes 1024 rows of a
-// pair, a thread four of them 256 rows apart.  Bound by the logits and weights
-// it reads and writes (4 G + 8 bytes a row).
+// w_r <- decay w_r + sum over heads of 2^(c d_r - m) / l: a CTA takes 1024 rows of a
+// pair, a thread four of them 256 rows apart.  Bound by the dot products and
+// weights it reads and writes (4 G + 8 bytes a row).
 constexpr int kWeightRows = 4 * kThreads;
 
-// V: logits per load, the largest of 4, 2, 1 that divides G.
+// V: dot products per load, the largest of 4, 2, 1 that divides G.
 template <int V>
 __global__ void __launch_bounds__(kThreads) kv_weights_kernel(const __grid_constant__ AttendArgs a, int chunks) {
   const int bh = blockIdx.x / chunks, r0 = (blockIdx.x - bh * chunks) * kWeightRows + threadIdx.x;
@@ -1153,8 +1163,8 @@ __global__ void __launch_bounds__(kThreads) kv_weights_kernel(const __grid_const
   sm100::grid_dep_wait();
   if (r0 >= len) return;
   const int n = a.G / V;
-  const float* lp = a.lse2 + (int64_t)bh * a.G;
-  const float* x = a.logits + ((int64_t)bh * a.c.max_len + r0) * a.G;
+  const float2* np = a.norm + (int64_t)bh * a.G;
+  const float* x = a.dots + ((int64_t)bh * a.c.max_len + r0) * a.G;
   float* w = a.w + bh * a.cap + r0;
   float old[4], p[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -1183,10 +1193,9 @@ __global__ void __launch_bounds__(kThreads) kv_weights_kernel(const __grid_const
     }
 #pragma unroll
     for (int g = 0; g < V; ++g) {
-      const float L = __ldcg(lp + k * V + g);
-      if (L != -INFINITY)  // else no row of the pair counts for this head
+      const float2 norm = __ldcg(np + k * V + g);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] += exp2f(v[i][g] - L);
+      for (int i = 0; i < 4; ++i) p[i] += weight_of(v[i][g], norm, a.scale2);
     }
   }
 #pragma unroll
@@ -1268,8 +1277,8 @@ cudaError_t launch_kv_attend(const Plan& p, const KvView& c, const void* q, int6
   a.decay = decay;
   a.scale2 = kLog2e / sqrtf((float)cfg.d_h);
   a.part = (float*)(base + L.part);
-  a.lse2 = (float*)(base + L.lse2);
-  a.logits = (float*)(base + L.logits);
+  a.norm = (float2*)(base + L.norm);
+  a.dots = (float*)(base + L.dots);
   const int unit = kSlotBytes / (cfg.d_h * p.esize);
   a.unit_log = unit == 64 ? 6 : unit == 32 ? 5 : 4;
   const int64_t most = a.BH * ceil_div64(c.max_len, unit);

@@ -356,7 +356,7 @@ typedef struct {
     size_t k_offset, v_offset;        /* bytes from the pool's base */
     size_t pool_bytes;
     size_t workspace_bytes;           /* kv_append, kv_evict, kv_decode_attention without weights */
-    size_t weights_workspace_bytes;   /* kv_decode_attention with weights (a logit per row and query head) */
+    size_t weights_workspace_bytes;   /* kv_decode_attention with weights (a float per row and query head) */
 } deltakv_kv_layout;
 
 /* One layer's plain paged cache as the kv calls take it; every pointer is the
