@@ -132,7 +132,7 @@ deltakv_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DELTAKV_OK :
 
 extern "C" {
 
-int32_t deltakv_version(void) { return 10000; }
+int32_t deltakv_version(void) { return 10100; }
 
 const char* deltakv_status_string(deltakv_status s) {
   switch (s) {

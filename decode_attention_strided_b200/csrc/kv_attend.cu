@@ -11,12 +11,12 @@
 // rounded by itself, would put 2^-19 into its weight, but m's rounding is the
 // same in numerator and denominator.
 //
-// Split: all pairs' rows, in units of 16 to 64 (8 KB of K), form one list that is cut into as
-// many equal ranges as there are CTAs, so that lengths do not matter for the
-// balance.  A CTA's range is a run of segments, each inside one pair; only
-// its first and its last segment can be a part of a pair, so a CTA leaves two
-// partial results at most.  A second kernel joins them and adds the weights,
-// which need the joined (m, l) of each head.
+// Split: all pairs' rows, in units of 16 to 64 (8 KB of K), form one list that
+// is cut into as many equal ranges as there are CTAs, so that lengths do not
+// matter for the balance.  A CTA's range is a run of segments, each inside one
+// pair; only its first and its last segment can be a part of a pair, so a CTA
+// leaves two partial results at most.  A second kernel joins them; a third adds
+// the weights, which need the joined (m, l) of each head.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -137,7 +137,7 @@ __device__ __forceinline__ Cut locate(const AttendArgs& a, int c, int* sh, int* 
       if (per > 1)
         for (;; ++b) {
           last = k.len(b);
-          if (target < s + units_of(last, a.unit_log)) break;
+          if (b + 1 == b1 || target < s + units_of(last, a.unit_log)) break;
           s += units_of(last, a.unit_log);
         }
       sh[kWarps] = b;
@@ -183,12 +183,15 @@ struct Merge {
   int bh[kBufs], slot[kBufs];  // whose part it is; partial slot, or -1 where the segment is the whole pair
 };
 
+// 1 / l, and 0 where no row counted.
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
 // Four dims of one head's result; the thread of a head's first dims also
 // writes its log-sum-exp (-inf where no row counted).
 template <int DH>
 __device__ __forceinline__ void write_out(const AttendArgs& a, int bh, int b, int h, int g, int e, float m, float l,
                                           float4 o) {
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = inverse_sum(l);
   *reinterpret_cast<float4*>(a.out + b * a.osb + (int64_t)(h * a.G + g) * a.osh + e) =
       make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
   if (e == 0) {
@@ -973,10 +976,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
   in.drain();
 }
 
-// The softmax weight of a row with dot product d (0 where no row of the pair
-// counts for the head).
+// The softmax weight of a row with dot product d; norm: (m, 1 / l).  Without a
+// maximum (m is -inf) no row counts for the head and 1 / l was set to 0, or the
+// rows that would are NaN and l is.
 __device__ __forceinline__ float weight_of(float d, float2 norm, float scale2) {
-  return norm.x == -INFINITY ? 0.f : exp2f(fmaf(d, scale2, -norm.x)) * norm.y;
+  return norm.x == -INFINITY ? norm.y : exp2f(fmaf(d, scale2, -norm.x)) * norm.y;
 }
 
 // Short rows: a cluster per pair, its CTAs equal runs of the pair's units, the
@@ -1062,7 +1066,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_short_kernel(const __gr
       for (int c = 0; c < C; ++c) m = fmaxf(m, peer(c)[kMaxG * DH + g]);
       const float mu = m == -INFINITY ? 0.f : m;
       for (int c = 0; c < C; ++c) l = fmaf(exp2f(peer(c)[kMaxG * DH + g] - mu), peer(c)[kMaxG * DH + kMaxG + g], l);
-      norm[g] = make_float2(m, 1.f / l);
+      norm[g] = make_float2(m, inverse_sum(l));
     }
     __syncthreads();
     for (int r = u0 * kRows + threadIdx.x; r < min(len, u1 * kRows); r += kThreads) {

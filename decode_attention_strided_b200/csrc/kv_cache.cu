@@ -14,8 +14,9 @@ namespace {
 
 // A warp copies the K and V rows 0 .. rows-1 of a group of kRows to pool rows
 // to(k) (skipped where that is negative): up to eight 16-byte words per lane
-// are loaded before the first is stored.  kWords: words of one row's K and V together (16, 32 or
-// 64); from(k, is_v): a row's address.  Both are called by all lanes alike.
+// are loaded before the first is stored.  kWords: words of one row's K and V
+// together (16, 32 or 64); from(k, is_v): a row's address.  Both are called by
+// all lanes alike.
 template <int kWords, int kRows, typename From, typename To>
 __device__ __forceinline__ void copy_rows(int rows, int lane, From from, To to, const KvView& c) {
   constexpr int kHalf = kWords / 2;
@@ -194,10 +195,13 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, int bh, int i0, in
   int64_t src = 0, dst = -1;
   if (lane < rows) {
     const int from = __ldcg(a.move + bh * a.half + i0 + lane), to = __ldcg(a.hole + bh * a.half + i0 + lane);
-    const int64_t s = a.c.row(bh, from), d = a.c.row(bh, to);
-    if (s >= 0 && d >= 0) src = s, dst = d;  // (a row without a place is neither read nor written)
-    a.w_out[bh * a.cap + to] = __ldcg(a.w + bh * a.cap + from);
-    a.pos_out[bh * a.cap + to] = __ldcg(a.pos + bh * a.cap + from);
+    // (always so, unless the weights changed under the call while the lists were made)
+    if ((uint32_t)from < (uint32_t)a.c.max_len && (uint32_t)to < (uint32_t)a.c.max_len) {
+      const int64_t s = a.c.row(bh, from), d = a.c.row(bh, to);
+      if (s >= 0 && d >= 0) src = s, dst = d;  // (a row without a place is neither read nor written)
+      a.w_out[bh * a.cap + to] = __ldcg(a.w + bh * a.cap + from);
+      a.pos_out[bh * a.cap + to] = __ldcg(a.pos + bh * a.cap + from);
+    }
   }
   __syncwarp();
   copy_rows<kWords, kRows>(

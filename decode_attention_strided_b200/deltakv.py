@@ -568,9 +568,9 @@ def set_profiling(p: Plan, enable: bool = True):
 
 def profile_collect(p: Plan) -> dict:
     """deltakv_profile_collect: {kernel name: (launches, total ms)}."""
-    buf = (_KernelTime * 16)()
+    buf = (_KernelTime * 32)()
     n = ctypes.c_int32()
-    _check("deltakv_profile_collect", load_library().deltakv_profile_collect(p.handle, buf, 16, ctypes.byref(n)))
+    _check("deltakv_profile_collect", load_library().deltakv_profile_collect(p.handle, buf, 32, ctypes.byref(n)))
     return {buf[i].name.decode(): (int(buf[i].launches), float(buf[i].total_ms)) for i in range(n.value)}
 
 

@@ -388,7 +388,8 @@ deltakv_status deltakv_kv_pool_layout(deltakv_plan_t plan, int32_t n_pages, int3
  * are left as they were.
  *   n_new      : tokens in K and V, 0 <= n_new (0 launches nothing)
  *   K, V       : device, element (b, h, t, e) at base + b*strides[0] +
- *                h*strides[1] + t*strides[2] + e, as for deltakv_compress
+ *                h*strides[1] + t*strides[2] + e, as for deltakv_compress;
+ *                outside the pool
  *   n_tokens   : device int32 [B] or NULL; a count outside [0, n_new], or
  *                larger than the pair's length, writes nothing for the pair
  *                and is reported as DEVICE_BOUNDS
@@ -413,7 +414,8 @@ deltakv_status deltakv_kv_append(deltakv_plan_t plan, const deltakv_kv_cache* ca
 /* Attention of one new token per sequence over its plain paged rows: for query
  * head hq of kv-head h,
  *   out = sum_r p_r V_r,  p = softmax_r(q . K_r / sqrt(d_h)),  r < lens[b][h]
- * (out = 0 and lse = -inf where a pair holds no row), and with weights also
+ * (out = 0, p = 0 and lse = -inf where a pair holds no row, or only rows whose
+ * logit is -inf), and with weights also
  *   weights[b][h][r] = decay weights[b][h][r] + sum over the pair's heads of p_r
  * for the same rows, the accumulated attention weight deltakv_kv_evict ranks
  * by.  Rows are split over the whole GPU whatever their lengths and joined by
@@ -436,8 +438,7 @@ deltakv_status deltakv_kv_decode_attention(deltakv_plan_t plan, const deltakv_kv
  * of a (sequence, kv-head), m = min(n, max(budget[b][h], n_first + n_recent))
  * are kept: those whose position is one of the first n_first (0 <= pos <
  * n_first) or of the last n_recent (pos > max pos - n_recent), then those with
- * the largest weights
- * (NaN ranks lowest; ties to the lower row).  Kept rows below m stay where
+ * the largest weights (NaN ranks lowest; ties to the lower row).  Kept rows below m stay where
  * they are; kept rows at or past m move, in order, into the dropped rows below
  * m, so that rows 0 .. m-1 are the kept ones and only what has to move moves
  * (attention does not depend on the rows' order; pos says which token a row

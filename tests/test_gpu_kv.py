@@ -156,6 +156,39 @@ def test_attend_infinities_and_nan_in_valid_rows_stay_in_their_pair(max_len, Hq,
     assert torch.isinf(got[:, 7]).all() and torch.isfinite(got[:, :7]).all() and torch.isfinite(got[:, 8:]).all()
 
 
+@pytest.mark.parametrize("max_len", [0, 40000], ids=["cluster", "cut"])
+@pytest.mark.parametrize("Hq,dtype", [(4, dkv.BF16), (6, dkv.BF16), (16, dkv.BF16), (4, dkv.F32)])
+def test_attend_logits_of_minus_infinity_and_nothing_but_nan(max_len, Hq, dtype):
+    """A pair whose logits are all -inf counts as one without rows, one where
+    some are is its other rows, and one that holds only NaN gives NaN."""
+    c = KvCase([[100, 100], [40, 1]], Hq, max_len=max_len, dtype=dtype)
+    s = Setup(c)
+    G = c.G
+    s.q.abs_()
+    dead = torch.zeros(100, dtype=torch.bool)
+    dead[::3] = dead[64:90] = True
+    for pair, rows in (((0, 0), torch.ones(100, dtype=torch.bool)), ((0, 1), dead)):
+        at = rows.nonzero()[:, 0]
+        s.pool[0, s.table_host[pair][at // c.page].long(), at % c.page] = float("-inf")
+    s.pool[0, s.table_host[1, 1, 0], 0] = float("nan")
+    out, lse, w = _attend(s, decay=0.5)
+    assert dkv.device_status(s.p, s.ws) == 0
+    _check_attend(s, out, lse, w, 0.5, pairs=[(1, 0)])
+    assert (out[0, :G] == 0).all() and (lse[0, :G] == float("-inf")).all()
+    assert torch.equal(w[0, 0].cpu()[:100], 0.5 * s.w[0, 0, :100])
+    for x in (out[1, G:], lse[1, G:], w[1, 1, :1]):
+        assert torch.isnan(x).all()
+    q, K, V = (x.double().numpy() for x in (s.q[0, G:], s.K[0, 1][~dead], s.V[0, 1][~dead]))
+    ref, ref_lse, p = attend64(q, K, V)
+    tol, tol_lse, rel = attend_bounds(q, K, V, p)
+    assert (np.abs(out[0, G:].cpu().numpy() - ref) <= tol).all()
+    assert (np.abs(lse[0, G:].cpu().numpy() - ref_lse) <= tol_lse).all()
+    want = torch.zeros(100, dtype=torch.float64)
+    want[~dead] = torch.from_numpy(p.sum(axis=0))
+    want += 0.5 * s.w[0, 1, :100].double()
+    assert ((w[0, 1].cpu()[:100].double() - want).abs() <= float(rel.max()) * want + 2.0 ** -22 * want).all()
+
+
 @pytest.mark.parametrize("max_len,page", [(300, 64), (40000, 64), (40000, 16), (300, 16)])
 def test_attend_bad_page_is_skipped_and_reported(max_len, page):
     c = KvCase([[300, 200], [300, 64]], 8, max_len=max_len, page=page)
@@ -563,3 +596,132 @@ def test_serving_steps_under_a_budget(dtype):
                 assert int(lens[b, h]) == m
                 assert torch.equal(w[b, h, :m].cpu(), w_mid[b, h][torch.from_numpy(src).long()])
         next_pos += 1
+
+
+@pytest.mark.parametrize("budget,prompt", [(96, 90), (3000, 2999)], ids=["short", "long"])
+def test_captured_serving_step_replays_like_eager_calls(budget, prompt):
+    """One append, attention with weights and eviction captured in a graph on a
+    side stream (passed explicitly), replayed for steps; the same steps eagerly
+    give the same bytes, the error word included."""
+    B, H, Hq, d, page = 2, 4, 16, 64, 32
+    cap = 6000 if budget > 1000 else 160
+    g = torch.Generator(device="cuda").manual_seed(4)
+    p = dkv.plan(dkv.Config(batch=B, kv_heads=H, q_heads=Hq, d_h=d, max_T=cap, stride_s=8, k=2, d_c=16, hidden=128))
+    per = -(-cap // page)
+    prompt_kv = torch.randn(2, B, H, prompt, d, generator=g, device="cuda").bfloat16()
+    steps = torch.randn(6, 3, B, max(H, Hq), 1, d, generator=g, device="cuda").bfloat16()
+    ends = []
+    for captured in (False, True):
+        pool = dkv.alloc_kv_pool(p, B * H * per, page)
+        table = torch.randperm(B * H * per, generator=torch.Generator().manual_seed(3)).to(torch.int32)
+        lens = torch.full((B, H), prompt, dtype=torch.int32, device="cuda")
+        cache = dkv.KVCache(p, pool, table.view(B, H, per).cuda(), lens)
+        ws = dkv.alloc_kv_workspace(p, cap, weights=True)
+        w = torch.zeros(B, H, cap, device="cuda")
+        pos = torch.zeros(B, H, cap, dtype=torch.int32, device="cuda")
+        bud = torch.full((B, H), budget, dtype=torch.int32, device="cuda")
+        at = torch.zeros(B, dtype=torch.int32, device="cuda")
+        dkv.kv_append(p, cache, cap, prompt_kv[0], prompt_kv[1], ws, first_pos=at, weights=w, pos=pos)
+        at += prompt
+        K, V, q = (torch.empty(B, n, 1, d, dtype=torch.bfloat16, device="cuda") for n in (H, H, Hq))
+        out, lse = torch.empty(B, Hq, d, device="cuda"), torch.empty(B, Hq, device="cuda")
+
+        def step(stream):
+            lens.add_(1)
+            dkv.kv_append(p, cache, cap, K, V, ws, first_pos=at, weights=w, pos=pos, stream=stream)
+            dkv.kv_decode_attention(p, cache, cap, q[:, :, 0], out, ws, weights=w, decay=0.95, lse=lse, stream=stream)
+            dkv.kv_evict(p, cache, cap, bud, w, pos, ws, n_first=1, n_recent=16, stream=stream)
+            at.add_(1)
+
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graph = None
+        outs = []
+        with torch.cuda.stream(side):
+            if captured:
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph, stream=side):
+                    step(side)
+            for i in range(len(steps)):
+                K.copy_(steps[i, 0, :, :H])
+                V.copy_(steps[i, 1, :, :H])
+                q.copy_(steps[i, 2, :, :Hq])
+                graph.replay() if captured else step(side)
+                outs.append((out.clone(), lse.clone()))
+        side.synchronize()
+        assert dkv.device_status(p, ws) == 0
+        assert (lens == min(budget, prompt + len(steps))).all()
+        ends.append([pool, w, pos, lens, at] + [x for o in outs for x in o])
+    for a, b in zip(*ends):
+        assert _same(a, b)
+
+
+def test_calls_on_another_device_than_the_current_one_are_refused():
+    s = Setup(KvCase([[10]], 1))
+    out = torch.empty(1, 1, 128, device="cuda")
+    s.cache.dev += 1  # as if the cache lived on another GPU
+    with pytest.raises(ValueError):
+        dkv.kv_decode_attention(s.p, s.cache, 10, s.q.cuda(), out, s.ws)
+
+
+def test_offsets_past_32_bits():
+    """The same append, attention and eviction with every array's used part
+    past 2^32 bytes (weights, positions, dot products: past 2^31 elements) as
+    with small ones: the same bytes."""
+    H, G, d, page = 9, 4, 128, 256
+    lens_host = torch.tensor([[0, 5000, 64, 1, 300, 17, 900, 33, 2000]], dtype=torch.int32)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    n = int(lens_host.max())
+    K, V = torch.randn(2, 1, H, n, d, generator=g, device="cuda").bfloat16()
+    q = torch.randn(1, H * G, d, generator=g, device="cuda").bfloat16()
+    tok_w = torch.rand(1, H, n, generator=g, device="cuda")
+    per = -(-n // page)
+    ends = []
+    for max_len, cap, n_pages, apart in ((40000, 40000, H * per, n * d), (1 << 26, 1 << 28, 66000, 1 << 28)):
+        p = dkv.plan(dkv.Config(batch=1, kv_heads=H, q_heads=H * G, d_h=d, max_T=1 << 26, stride_s=8, k=2, d_c=16,
+                                hidden=128))
+        pool = torch.empty(2, n_pages, page, d, dtype=torch.bfloat16, device="cuda")
+        table = torch.full((1, H, -(-max_len // page)), -1, dtype=torch.int32)
+        table[:, :, :per] = n_pages - 1 - torch.arange(H * per).view(1, H, per)
+        lens = lens_host.cuda()
+        cache = dkv.KVCache(p, pool, table.cuda(), lens)
+        ws = dkv.alloc_kv_workspace(p, max_len, weights=True)
+        w = torch.empty(1, H, cap, device="cuda")
+        pos = torch.empty(1, H, cap, dtype=torch.int32, device="cuda")
+        src = torch.empty(H * apart, dtype=torch.bfloat16, device="cuda")
+        Ks = src.as_strided((1, H, n, d), (0, apart, d, 1))
+        at = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = torch.empty(1, H * G, d, device="cuda"), torch.empty(1, H * G, device="cuda")
+        # a call per pair: the last lens rows of the others would be written too, so their counts are theirs
+        Ks.copy_(K)
+        for h in range(H):
+            m = int(lens_host[0, h])
+            only = torch.zeros_like(lens)
+            only[0, h] = m
+            one = dkv.KVCache(p, pool, cache.page_table, only)
+            count = torch.full((1,), m, dtype=torch.int32, device="cuda")
+            dkv.kv_append(p, one, max_len, Ks, Ks, ws, n_tokens=count, first_pos=at, weights=w, pos=pos,
+                          token_weights=tok_w)
+            dkv.device_status(p, ws)  # (the other pairs have no room for m tokens: reported, not written)
+        for h in range(H):
+            ids = table[0, h, :per].long().cuda()
+            rows = pool[:, ids].view(2, -1, d)
+            m = int(lens_host[0, h])
+            assert torch.equal(rows[0, :m], K[0, h, :m]) and torch.equal(rows[1, :m], K[0, h, :m])
+        pool[1, table[:, :, :per].reshape(-1).long().cuda()] = V.new_tensor(0.5)
+        dkv.kv_decode_attention(p, cache, max_len, q, out, ws, weights=w, decay=0.9, lse=lse)
+        used = [w[0, h, :int(lens_host[0, h])].clone() for h in range(H)]
+        budget = (lens_host // 2).cuda()
+        dkv.kv_evict(p, cache, max_len, budget, w, pos, ws, n_first=1, n_recent=2)
+        assert dkv.device_status(p, ws) == 0
+        kept = []
+        for h in range(H):
+            m = int(lens[0, h])
+            assert m == min(int(lens_host[0, h]), max(int(lens_host[0, h]) // 2, 3))
+            ids = table[0, h, :per].long().cuda()
+            kept += [pool[0, ids].view(-1, d)[:m].clone(), w[0, h, :m].clone(), pos[0, h, :m].clone()]
+            assert torch.equal(kept[-3], K[0, h][kept[-1].long()])
+        ends.append([out, lse] + used + kept)
+        del pool, w, pos, src, Ks, ws, cache, one
+    for a, b in zip(*ends):
+        assert _same(a, b)
