@@ -673,7 +673,8 @@ struct Bf16Rows {
 // head's query in registers (64 at most: kL is 4 to 16 by the heads); the GP
 // heads' partial sums are reduced over the kL lanes by exchange steps that
 // leave each lane one head.  Outputs: a lane holds four dims of all heads and
-// reads the rows' weights from shared memory.
+// reads the rows' weights from shared memory.  Bound by issue: d_h 64, eight
+// heads, 226 MB 48 us (4.7 TB/s; 76 us with 32 lanes per row).
 // GP: heads rounded up to a power of two.
 template <int DH, int GP_>
 struct F32Rows {
@@ -913,7 +914,9 @@ __device__ __forceinline__ void init_ring(RingSmem& ring, int warp, int lane) {
   if (threadIdx.x == 0) ring.dead = 0;
 }
 
-// One CTA per SM, eight warps with a ring each.
+// One CTA per SM, eight warps with a ring each.  bf16, d_h 128, four heads: 64
+// pairs of 131072 rows (4.3 GB) 607 us, 7.1 TB/s, in a short run; 665 us, 6.5
+// TB/s, in a long one under the power limit.
 template <int DH, typename Rows>
 __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_constant__ AttendArgs a) {
   using E = typename Rows::E;
@@ -1087,8 +1090,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_short_kernel(const __gr
 // A warp takes cp words of four outputs, its lanes beyond those the parts in
 // turn: a lane loads its parts' (m, l, o) at once and folds them, then the
 // lanes of the same word fold (a fixed order: the result does not depend on
-// timing).  One round trip to L2 after the attention's end; the search for the
-// cut runs before it.
+// timing).  One round trip to L2 after the attention's end, the search for the
+// cut runs before it: 3.5 us with the launch, whatever the lengths.
 template <int DH>
 __global__ void __launch_bounds__(kThreads) kv_join_kernel(const __grid_constant__ AttendArgs a) {
   __shared__ int sh_loc[kLocateWords];
@@ -1156,7 +1159,8 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(const __grid_constant
 
 // w_r <- decay w_r + sum over heads of 2^(c d_r - m) / l: a CTA takes 1024 rows of a
 // pair, a thread four of them 256 rows apart.  Bound by the dot products and
-// weights it reads and writes (4 G + 8 bytes a row).
+// weights it reads and writes (4 G + 8 bytes a row): 64 pairs of 2048 to 16384
+// rows, G = 4, 4 to 5 us.
 constexpr int kWeightRows = 4 * kThreads;
 
 // V: dot products per load, the largest of 4, 2, 1 that divides G.

@@ -416,9 +416,11 @@ def _kv_meta(name, t, dtype, pairs, dev):
     """A [B, H, cap] array of row weights or positions: (pointer, cap)."""
     if not isinstance(t, torch.Tensor) or t.dim() != 3:
         raise ValueError(f"{name} must be a tensor {list(pairs) + ['cap']}")
-    cap = t.shape[2]
+    b, h, cap = t.shape
     if cap > 0x7fffffff:
         raise ValueError(f"{name}: cap does not fit 32 bits")
+    if (b, h) == pairs and t.dtype is dtype and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr(), cap
     return _kv_tensor(name, t, dtype, (*pairs, cap), dev), cap
 
 
@@ -454,6 +456,7 @@ class KVCache:
         lp = _kv_tensor("lens", lens, torch.int32, (c.batch, c.kv_heads), self.dev)
         self.plan, self.pool, self.page_table, self.lens = p, pool, page_table, lens
         self._fields = (pp, n_pages, page, tp, max_pages, lp)
+        self._view = _KvCache(*self._fields, 1)
 
     def _call(self, fn, p, max_len, workspace, stream):
         """What every kv call passes: the C view, the workspace, its bytes and
@@ -470,8 +473,10 @@ class KVCache:
             stream = torch._C._cuda_getCurrentRawStream(self.dev)
         elif hasattr(stream, "cuda_stream"):
             stream = stream.cuda_stream
-        # a view of its own for each call: max_len belongs to the call
-        return _KvCache(*self._fields, max_len), workspace.data_ptr(), workspace.nbytes, int(stream)
+        view = self._view
+        if view.max_len != max_len:  # a view is never changed: another thread's call may be reading it
+            view = self._view = _KvCache(*self._fields, max_len)
+        return view, workspace.data_ptr(), workspace.nbytes, int(stream)
 
 
 def kv_append(p: Plan, cache: KVCache, max_len: int, K, V, workspace, n_tokens=None, first_pos=None, weights=None,

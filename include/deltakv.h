@@ -365,6 +365,11 @@ typedef struct {
  * [0, max_len] is read as 0; both are reported as DELTAKV_ERR_DEVICE_BOUNDS.
  * Entries of page_table past a pair's last page are not read.  Calls that
  * write rows (append, evict) need each of the pages to be in the table once.
+ * The first 16 bytes of a workspace are zero before its first call
+ * (deltakv_device_status leaves them so); the rest belongs to one call at a
+ * time: calls that can run at once (on several streams, in graphs replayed on
+ * several) take a workspace each, and none of them may write what another
+ * reads.
  * UNSUPPORTED: B H ceil(max_len / 16) of 2^31 and more. */
 typedef struct {
     void* pool;                 /* device, 16-byte aligned, pool_bytes */
@@ -438,11 +443,11 @@ deltakv_status deltakv_kv_decode_attention(deltakv_plan_t plan, const deltakv_kv
  * of a (sequence, kv-head), m = min(n, max(budget[b][h], n_first + n_recent))
  * are kept: those whose position is one of the first n_first (0 <= pos <
  * n_first) or of the last n_recent (pos > max pos - n_recent), then those with
- * the largest weights (NaN ranks lowest; ties to the lower row).  Kept rows below m stay where
- * they are; kept rows at or past m move, in order, into the dropped rows below
- * m, so that rows 0 .. m-1 are the kept ones and only what has to move moves
- * (attention does not depend on the rows' order; pos says which token a row
- * is).  K and V rows move in place.  Pages past ceil(m / tokens_per_page) are
+ * the largest weights (NaN ranks lowest; ties to the lower row).  Kept rows
+ * below m stay where they are; kept rows at or past m move, in order, into the
+ * dropped rows below m, so that rows 0 .. m-1 are the kept ones and only what
+ * has to move moves (attention does not depend on the rows' order; pos says
+ * which token a row is).  K and V rows move in place.  Pages past ceil(m / tokens_per_page) are
  * free afterwards.
  *   budget     : device int32 [B][H]; a negative entry drops nothing and is
  *                reported as DEVICE_BOUNDS

@@ -725,3 +725,41 @@ def test_offsets_past_32_bits():
         del pool, w, pos, src, Ks, ws, cache, one
     for a, b in zip(*ends):
         assert _same(a, b)
+
+
+def test_two_threads_share_a_cache():
+    """Two host threads, each with a stream, a workspace and a max_len (so a
+    form of the attention) of its own, read one cache at once."""
+    import threading
+
+    s = Setup(KvCase([[500, 17], [64, 900]], 8, max_len=40000))
+    q = s.q.cuda()
+    bounds = (900, 40000)
+    outs = [[torch.full((2, 8, 128), float("nan"), device="cuda") for _ in range(40)] for _ in bounds]
+    wss = [dkv.alloc_kv_workspace(s.p, n) for n in bounds]
+    want = []
+    for n, ws in zip(bounds, wss):
+        out = torch.empty(2, 8, 128, device="cuda")
+        dkv.kv_decode_attention(s.p, s.cache, n, q, out, ws)
+        want.append(out)
+    torch.cuda.synchronize()
+    failed = []
+
+    def calls(i):
+        try:
+            stream = torch.cuda.Stream()
+            for out in outs[i]:
+                dkv.kv_decode_attention(s.p, s.cache, bounds[i], q, out, wss[i], stream=stream)
+            stream.synchronize()
+        except Exception as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=calls, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for o, ref, ws in zip(outs, want, wss):
+        assert dkv.device_status(s.p, ws) == 0
+        assert all(torch.equal(x, ref) for x in o)
