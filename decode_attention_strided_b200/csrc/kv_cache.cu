@@ -110,14 +110,14 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) kv_append_kernel(const _
 // (movers), of which there are equally many: mover i goes to hole i.  Bound by
 // its chain of block and cluster barriers, the keys are read once: 8 pairs of
 // 131072 rows 29 us, 64 pairs of 4096 to 32768 rows 20 us.
-// Where the moves are few for certain, the clusters make them; else a second
+// Where the rows per thread are few, the clusters make the moves; else a second
 // kernel does, spread over the whole GPU whatever the pairs' shares: bound by
 // the rows read and written.
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBinBits = 10;
 constexpr int kBins = 1 << kBinBits;
-constexpr int kPerSmall = 2, kPerLarge = 16;  // rows per thread in registers
+constexpr int kPerLarge = 16;         // rows per thread in registers, at most
 constexpr int kMaxCluster = 8;
 constexpr int kFew = 4;               // this many rows to drop are found one by one
 static_assert(kBins == kSelThreads && kSelWarps == 32, "a thread per bin, a lane per warp");
@@ -671,6 +671,29 @@ cudaError_t launch_kv_append(const Plan& p, const KvView& c, int n_new, const KV
   return launch_pdl(kern, grid, kAppendWarps * 32, 0, st, a);
 }
 
+// CTAs per pair: as many as find room at once, one to an SM (16 clusters of eight
+// and 36 of four do not, 32 of four and 72 of two do; us replayed, half of the
+// rows dropped: 16 pairs of 15000 by eight / four 42 / 34, 36 pairs by four / two
+// 70 / 52, 72 pairs by two / one 74 / 78), each with 512 rows at least, and one
+// below 2048 rows (8 pairs, half dropped, 512 / 1024 rows at least: 2049 rows
+// 15.3 / 17.2, 4000 rows 17.3 / 21.4; one of 1100 rows dropped by one / two 5.8 /
+// 7.6).
+constexpr int kMinRun = 512, kMinSplit = 2048;
+constexpr int select_ctas(int cluster) { return cluster == 8 ? 96 : cluster == 4 ? 128 : kNumSMs; }
+
+// The clusters make the moves themselves, without a second kernel, where their
+// threads hold 4 rows at most, and up to 8 where two thirds of the SMs take part.
+// us replayed, here / second kernel: one row dropped, 32 pairs of 15000 (4 rows)
+// 9.5 / 15.9, 64 of 15000 (8 rows) 11.1 / 17.1; half dropped 40 / 49 and 70 / 74, 16
+// of 32000 (8 rows on 64 SMs) 63 / 52, 64 of 32000 (16 rows) 140 / 127 and twice
+// that where lengths differ.
+constexpr int kHere = 4, kHereMany = 8, kManyCtas = 96;
+
+template <int kPer>
+auto select_here(int words) {
+  return words == 16 ? kv_select_kernel<kPer, 16> : words == 32 ? kv_select_kernel<kPer, 32> : kv_select_kernel<kPer, 64>;
+}
+
 cudaError_t launch_kv_evict(const Plan& p, const KvView& c, const int32_t* budget, int n_first, int n_recent,
                             const float* w, const int32_t* pos, float* w_out, int32_t* pos_out, int cap,
                             int32_t* lens_out, void* ws, cudaStream_t st) {
@@ -691,20 +714,19 @@ cudaError_t launch_kv_evict(const Plan& p, const KvView& c, const int32_t* budge
   a.hole = (int32_t*)((char*)ws + L.hole);
   a.move = (int32_t*)((char*)ws + L.move);
   a.half = c.max_len / 2;
-  // as many CTAs per pair as the SMs hold at once (one each), each with 1024 rows at least
   a.cluster = 1;
-  while (a.cluster < kMaxCluster && (int64_t)a.BH * a.cluster * 2 <= kNumSMs && a.cluster * 2 * 1024 <= c.max_len)
-    a.cluster *= 2;
+  if (c.max_len >= kMinSplit)
+    while (a.cluster < kMaxCluster && (int64_t)a.BH * a.cluster * 2 <= select_ctas(a.cluster * 2) &&
+           a.cluster * 2 * kMinRun <= c.max_len)
+      a.cluster *= 2;
   const int run = (int)ceil_div64(c.max_len, a.cluster);
   const int words = p.cfg.d_h * p.esize / 8;
-  // At most half the rows move.  With 2048 rows per CTA the clusters make the moves in no more time than the second
-  // kernel does, launch included (us replayed, here / second kernel: 64 pairs of 4096 rows, half of them dropped 35 /
-  // 38, 96 dropped 18 / 25; 8 pairs 20 / 20 and 16 / 20), and the host saves a launch.
-  const bool all_here = run <= kPerSmall * kSelThreads;
-  auto select = !all_here     ? kv_select_kernel<kPerLarge, 0>
-                : words == 16 ? kv_select_kernel<kPerSmall, 16>
-                : words == 32 ? kv_select_kernel<kPerSmall, 32>
-                              : kv_select_kernel<kPerSmall, 64>;
+  const int per = (int)ceil_div64(run, kSelThreads);
+  const bool all_here = per <= kHere || (per <= kHereMany && a.BH * a.cluster >= kManyCtas);
+  auto select = !all_here      ? kv_select_kernel<kPerLarge, 0>
+                : per <= 2     ? select_here<2>(words)
+                : per <= kHere ? select_here<kHere>(words)
+                               : select_here<kHereMany>(words);
   cudaError_t e;
   {
     ProfScope ps(p, st, KID_KV_SELECT);

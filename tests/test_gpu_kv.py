@@ -471,6 +471,33 @@ def test_evict(name, case, div, first, recent, kind, in_place):
     assert _evict_check(s, budget, first, recent, w, pos, in_place) == 0
 
 
+def _few_long(n, pairs):
+    """`pairs` pairs, one of n rows and one of n - 1, the others short."""
+    return [[n if b == 1 else n - 1 if b == 3 else 3 + b % 60] for b in range(pairs)]
+
+
+# rows per thread of the selection (4, 8, 16) and row sizes; who makes the moves
+EVICT_FORMS = [
+    ("4_bf16", KvCase([[17000], [30011]], 1, page=128)),
+    ("4_f32", KvCase([[17003, 2]], 2, page=256, dtype=dkv.F32)),
+    ("8_bf16_d64", KvCase(_few_long(7001, 100), 1, d=64)),
+    ("8_bf16", KvCase(_few_long(13001, 60), 1)),
+    ("8_f32", KvCase(_few_long(6001, 100), 1, dtype=dkv.F32)),
+    ("16_bf16", KvCase([[70003], [65000]], 1, page=256)),
+    ("16_f32", KvCase([[66001]], 1, page=256, dtype=dkv.F32)),
+]
+
+
+@pytest.mark.parametrize("kind", ["random", "equal", "special"])
+@pytest.mark.parametrize("drop", ["two", "half"])
+@pytest.mark.parametrize("name,case", EVICT_FORMS, ids=[e[0] for e in EVICT_FORMS])
+def test_evict_forms(name, case, drop, kind):
+    s = Setup(case)
+    w, pos = _meta(case, 5, kind, case.n)
+    budget = [[max(0, n - 2) if drop == "two" else n // 2 for n in row] for row in case.lens]
+    assert _evict_check(s, budget, 2, 30, w, pos, True) == 0
+
+
 def test_evict_budgets_of_nothing_everything_and_out_of_range():
     c = KvCase([[300, 301, 302, 303]], 4)
     s = Setup(c)
