@@ -915,8 +915,8 @@ __device__ __forceinline__ void init_ring(RingSmem& ring, int warp, int lane) {
 }
 
 // One CTA per SM, eight warps with a ring each.  bf16, d_h 128, four heads: 64
-// pairs of 131072 rows (4.3 GB) 607 us, 7.1 TB/s, in a short run; 665 us, 6.5
-// TB/s, in a long one under the power limit.
+// pairs of 131072 rows (4.3 GB) 607 us, 7.1 TB/s, in a short run; 628 to 682 us,
+// 6.3 to 6.8 TB/s, in a long one under the power limit.
 template <int DH, typename Rows>
 __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_constant__ AttendArgs a) {
   using E = typename Rows::E;
