@@ -790,3 +790,46 @@ def test_two_threads_share_a_cache():
     for o, ref, ws in zip(outs, want, wss):
         assert dkv.device_status(s.p, ws) == 0
         assert all(torch.equal(x, ref) for x in o)
+
+
+FIRST_CALLS = """
+import sys
+import torch
+from decode_attention_strided_b200 import deltakv as dkv
+n, B, H, Hq, d = int(sys.argv[1]), 1, 4, 8, 128
+per = -(-n // 64)
+p = dkv.plan(dkv.Config(batch=B, kv_heads=H, q_heads=Hq, d_h=d, max_T=n, stride_s=8, k=2, d_c=16, hidden=128))
+pool = dkv.alloc_kv_pool(p, H * per, 64)
+table = torch.arange(H * per, dtype=torch.int32, device="cuda").view(B, H, per)
+lens = torch.full((B, H), n, dtype=torch.int32, device="cuda")
+cache = dkv.KVCache(p, pool, table, lens)
+ws = dkv.alloc_kv_workspace(p, n, weights=True)
+w, at = torch.zeros(B, H, n, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+pos = torch.zeros(B, H, n, dtype=torch.int32, device="cuda")
+K = torch.randn(B, H, n, d, device="cuda").bfloat16()
+q, out = torch.randn(B, Hq, d, device="cuda").bfloat16(), torch.zeros(B, Hq, d, device="cuda")
+budget = torch.full((B, H), n // 2, dtype=torch.int32, device="cuda")
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    dkv.kv_append(p, cache, n, K, K, ws, first_pos=at, weights=w, pos=pos)
+    dkv.kv_decode_attention(p, cache, n, q, out, ws, weights=w)
+    dkv.kv_evict(p, cache, n, budget, w, pos, ws, n_recent=4)
+g.replay()
+torch.cuda.synchronize()
+x = (q.float().view(B, H, 2, d) @ K.float().transpose(-1, -2)) / d ** 0.5
+ref = (x.softmax(-1) @ K.float()).reshape(B, Hq, d)
+# (float32 on both sides: 2^-8 of rows near 1 is far above their rounding, far below a wrong row)
+assert (out - ref).abs().max() < 2 ** -8, (out - ref).abs().max()
+assert (lens == n // 2).all() and dkv.device_status(p, ws) == 0
+"""
+
+
+@pytest.mark.parametrize("n", [300, 70001], ids=["short", "long"])
+def test_first_calls_of_a_process_may_be_captured(n):
+    import pathlib
+    import subprocess
+    import sys
+
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS, str(n)], cwd=pathlib.Path(__file__).parent.parent,
+                       capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr[-2000:]
