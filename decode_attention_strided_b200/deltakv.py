@@ -441,22 +441,69 @@ class KVCache:
     """One layer's plain paged cache (deltakv_kv_cache): pool [2, n_pages,
     tokens_per_page, d_h] in the plan's type, page_table int32 [B, H,
     max_pages], lens int32 [B, H] (valid rows).  Holds the tensors; the caller
-    may change their contents between calls."""
+    may change their contents between calls, and may assign another pool,
+    page_table or lens, which is checked like the first one and used from the
+    next call on (a graph keeps the tensors that it was captured with)."""
 
     def __init__(self, p: Plan, pool, page_table, lens):
+        self._bind(p, pool, page_table, lens)
+
+    def _bind(self, p, pool, page_table, lens):
         c = p.cfg
         if not isinstance(pool, torch.Tensor) or pool.dim() != 4:
             raise ValueError("pool must be a tensor [2, n_pages, tokens_per_page, d_h]")
         n_pages, page = int(pool.shape[1]), int(pool.shape[2])
         kv_pool_layout(p, n_pages, page, 1)
-        self.dev = pool.get_device()
-        pp = _kv_tensor("pool", pool, c.torch_dtype(), (2, n_pages, page, c.d_h), self.dev)
+        dev = pool.get_device()
+        pp = _kv_tensor("pool", pool, c.torch_dtype(), (2, n_pages, page, c.d_h), dev)
+        if not isinstance(page_table, torch.Tensor):
+            raise TypeError("page_table: expected a torch tensor")
         max_pages = _page_table(p, page_table)
-        tp = _kv_tensor("page_table", page_table, torch.int32, (c.batch, c.kv_heads, max_pages), self.dev)
-        lp = _kv_tensor("lens", lens, torch.int32, (c.batch, c.kv_heads), self.dev)
-        self.plan, self.pool, self.page_table, self.lens = p, pool, page_table, lens
-        self._fields = (pp, n_pages, page, tp, max_pages, lp)
-        self._view = _KvCache(*self._fields, 1)
+        tp = _kv_tensor("page_table", page_table, torch.int32, (c.batch, c.kv_heads, max_pages), dev)
+        lp = _kv_tensor("lens", lens, torch.int32, (c.batch, c.kv_heads), dev)
+        self.plan, self.dev = p, dev
+        # replaced as a whole, never changed: another thread's call may be reading them
+        fields = (pp, n_pages, page, tp, max_pages, lp)
+        self._bound = (pool, page_table, lens, fields)
+        self._last = (fields, 1, _KvCache(*fields, 1))
+        return fields
+
+    @property
+    def pool(self):
+        return self._bound[0]
+
+    @pool.setter
+    def pool(self, t):
+        self._bind(self.plan, t, self.page_table, self.lens)
+
+    @property
+    def page_table(self):
+        return self._bound[1]
+
+    @page_table.setter
+    def page_table(self, t):
+        self._bind(self.plan, self.pool, t, self.lens)
+
+    @property
+    def lens(self):
+        return self._bound[2]
+
+    @lens.setter
+    def lens(self, t):
+        self._bind(self.plan, self.pool, self.page_table, t)
+
+    def _view(self, max_len):
+        """The C view of the tensors as they are now (their storage may have
+        been replaced, by set_ or .data); made anew only where it differs from
+        the last call's."""
+        pool, table, lens, fields = self._bound
+        if pool.data_ptr() != fields[0] or table.data_ptr() != fields[3] or lens.data_ptr() != fields[5]:
+            fields = self._bind(self.plan, pool, table, lens)
+        of, n, view = self._last
+        if of is not fields or n != max_len:
+            view = _KvCache(*fields, max_len)
+            self._last = (fields, max_len, view)
+        return view
 
     def _call(self, fn, p, max_len, workspace, stream):
         """What every kv call passes: the C view, the workspace, its bytes and
@@ -465,7 +512,7 @@ class KVCache:
             raise DeltaKVError(fn, 1)
         if self.plan is not p and self.plan.cfg != p.cfg:
             raise ValueError("the cache belongs to a plan of another configuration")
-        if self.dev < 0 or self.dev != torch.cuda.current_device():
+        if self.dev < 0 or self.dev != torch._C._cuda_getDevice():
             raise ValueError(f"the cache is on {self.pool.device}, not on the current CUDA device")
         if workspace.get_device() != self.dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor where the cache is")
@@ -473,10 +520,7 @@ class KVCache:
             stream = torch._C._cuda_getCurrentRawStream(self.dev)
         elif hasattr(stream, "cuda_stream"):
             stream = stream.cuda_stream
-        view = self._view
-        if view.max_len != max_len:  # a view is never changed: another thread's call may be reading it
-            view = self._view = _KvCache(*self._fields, max_len)
-        return view, workspace.data_ptr(), workspace.nbytes, int(stream)
+        return self._view(max_len), workspace.data_ptr(), workspace.nbytes, int(stream)
 
 
 def kv_append(p: Plan, cache: KVCache, max_len: int, K, V, workspace, n_tokens=None, first_pos=None, weights=None,

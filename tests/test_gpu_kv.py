@@ -833,3 +833,31 @@ def test_first_calls_of_a_process_may_be_captured(n):
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS, str(n)], cwd=pathlib.Path(__file__).parent.parent,
                        capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_assigned_tensors_are_the_ones_that_are_read_and_written():
+    """Lengths, pages and pool assigned to a cache are what the next calls
+    use; eviction in place writes the lengths that it read."""
+    c = KvCase([[300, 200], [40, 129]], 8)
+    s = Setup(c)
+    fresh = Setup(dataclasses.replace(c, seed=1))
+    other = dkv.KVCache(s.p, fresh.pool, fresh.table, fresh.lens)
+    first_lens, first_table, first_pool = other.lens, other.page_table, other.pool  # (kept: none is freed)
+    other.pool, other.page_table, other.lens = s.pool, s.table, s.lens - 0
+    out, lse, w = _attend(s)
+    s.cache = other
+    for a, b in zip((out, lse, w), _attend(s)):
+        assert _same(a, b)
+    other.lens = less = s.lens // 2
+    half = Setup.__new__(Setup)
+    half.__dict__.update(s.__dict__)
+    half.c = dataclasses.replace(c, lens=less.tolist(), max_len=c.n)
+    half.K = {k: v[:half.c.lens[k[0]][k[1]]] for k, v in s.K.items()}
+    half.V = {k: v[:half.c.lens[k[0]][k[1]]] for k, v in s.V.items()}
+    _check_attend(half, *_attend(s))
+    wd, pos = s.w.cuda(), torch.arange(c.n, dtype=torch.int32, device="cuda").expand(2, 2, c.n).contiguous()
+    dkv.kv_evict(s.p, other, c.n, torch.full((2, 2), 11, dtype=torch.int32, device="cuda"), wd, pos, s.ws)
+    assert dkv.device_status(s.p, s.ws) == 0
+    assert (less == 11).all() and other.lens is less
+    assert torch.equal(s.lens.cpu(), s.lens_host) and torch.equal(first_lens.cpu(), fresh.lens_host)
+    assert _same(first_pool, Setup(dataclasses.replace(c, seed=1)).pool) and first_table is fresh.table

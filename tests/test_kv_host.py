@@ -219,3 +219,45 @@ def test_the_plain_implementations():
     assert m == 3 and src.tolist() == [0, 1, 2]
     m, src = evict64(4, 2, 0, 0, np.array([np.nan, -np.inf, np.nan, 1], np.float32), np.arange(4))
     assert m == 2 and src.tolist() == [3, 1]
+
+
+def _pointers(view):
+    return view.pool, view.n_pages, view.tokens_per_page, view.page_table, view.max_pages, view.lens, view.max_len
+
+
+def _of(pool, table, lens, max_len):
+    return (pool.data_ptr(), pool.shape[1], pool.shape[2], table.data_ptr(), table.shape[2], lens.data_ptr(), max_len)
+
+
+def test_a_cache_passes_the_tensors_it_shows(lib):
+    """Assigning pool, page_table or lens takes effect, as does replacing the
+    storage of one; what the constructor refuses is refused, with the cache
+    left as it was."""
+    p = _plan()
+    pool, table, lens = _cpu_cache(p)
+    cache = dkv.KVCache(p, pool, table, lens)
+    assert _pointers(cache._view(10)) == _of(pool, table, lens, 10)
+    held = cache._view(10)
+    cache.lens = more = lens + 1
+    assert cache.lens is more and _pointers(cache._view(10)) == _of(pool, table, more, 10)
+    assert _pointers(held) == _of(pool, table, lens, 10)  # a view in another thread's hands stays what it was
+    cache.page_table = wide = torch.zeros(2, 2, 20, dtype=torch.int32)
+    cache.pool = small = torch.zeros(2, 9, 128, 128, dtype=torch.bfloat16)
+    for max_len in (1000, 10, 10):
+        assert _pointers(cache._view(max_len)) == _of(small, wide, more, max_len)
+    for name, bad in (("pool", small.float()), ("pool", small[0]), ("pool", None), ("page_table", wide.long()),
+                      ("page_table", wide[..., ::2]), ("page_table", 3), ("lens", lens[0]), ("lens", lens.float()),
+                      ("lens", "lens")):
+        with pytest.raises((ValueError, TypeError)):
+            setattr(cache, name, bad)
+        assert _pointers(cache._view(10)) == _of(small, wide, more, 10)
+        assert cache.pool is small and cache.page_table is wide and cache.lens is more
+    moved = torch.ones(2, 2, dtype=torch.int32)
+    more.set_(moved)
+    assert _pointers(cache._view(10)) == _of(small, wide, moved, 10)
+    bigger = torch.zeros(2, 30, 128, 128, dtype=torch.bfloat16)
+    small.data = bigger
+    assert _pointers(cache._view(10)) == _of(bigger, wide, moved, 10)
+    more.set_(torch.ones(2, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        cache._view(10)
