@@ -579,7 +579,8 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
   }
   if (rank == 0 && tid == 0) {
     a.count[bh] = cnt;
-    a.lens_out[bh] = m;
+    // in place, a length out of range stays the caller's: 0 would lose the rows for good
+    if (raw == n || a.lens_out != a.c.lens) a.lens_out[bh] = m;
   }
 }
 

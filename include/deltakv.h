@@ -455,7 +455,8 @@ deltakv_status deltakv_kv_decode_attention(deltakv_plan_t plan, const deltakv_kv
  *   weights, pos : device float32 and int32 [B][H][cap], cap >= max_len
  *   weights_out, pos_out : device [B][H][cap], rows 0 .. m-1 are written;
  *                each may be its input (in place), else must not overlap it
- *   lens_out   : device int32 [B][H], set to m; may be cache->lens
+ *   lens_out   : device int32 [B][H], set to m; may be cache->lens, of which
+ *                an entry out of range then stays as it is
  *   workspace  : workspace_bytes of the layout for this max_len.
  * A pair with a page index out of range among its first n rows is left whole
  * (m = n) and reported.  Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT,

@@ -861,3 +861,26 @@ def test_assigned_tensors_are_the_ones_that_are_read_and_written():
     assert (less == 11).all() and other.lens is less
     assert torch.equal(s.lens.cpu(), s.lens_host) and torch.equal(first_lens.cpu(), fresh.lens_host)
     assert _same(first_pool, Setup(dataclasses.replace(c, seed=1)).pool) and first_table is fresh.table
+
+
+@pytest.mark.parametrize("bad", [-1, 301, 2**31 - 1])
+@pytest.mark.parametrize("n", [300, 5000], ids=["block", "cluster"])
+def test_evict_in_place_leaves_a_length_out_of_range_as_it_is(n, bad):
+    """The pair's rows, weights, positions and length are all as before; the
+    other pairs are evicted, and a second call with the length put right too."""
+    c = KvCase([[n, 200, 129]], 3, max_len=n)
+    s = Setup(c)
+    w, pos = _meta(c, 4, "random")
+    wrong = n + 1 if bad == 301 else bad
+    s.lens[0, 0] = wrong
+    pool0, wd, pd = s.pool.cpu(), w.cuda(), pos.cuda()
+    budget = torch.full((1, 3), 100, dtype=torch.int32, device="cuda")
+    dkv.kv_evict(s.p, s.cache, n, budget, wd, pd, s.ws)
+    assert dkv.device_status(s.p, s.ws) == BOUNDS
+    assert s.lens.tolist() == [[wrong, 100, 100]]
+    ids = s.table_host[0, 0, :-(-n // c.page)].long()
+    assert _same(s.pool[:, ids.cuda()], pool0[:, ids]) and _same(wd[0, 0], w[0, 0]) and _same(pd[0, 0], pos[0, 0])
+    s.lens[0, 0] = n
+    s.c = KvCase([[n, 100, 100]], 3, max_len=n)
+    s.lens_host = torch.tensor(s.c.lens, dtype=torch.int32)
+    assert _evict_check(s, [[100, 100, 100]], 0, 0, wd.cpu(), pd.cpu(), True) == 0
