@@ -60,9 +60,11 @@ deltakv_status make_view(const Plan& p, const deltakv_kv_cache* c, void* workspa
   deltakv_status st = check_pool(c->n_pages, c->tokens_per_page);
   if (st != DELTAKV_OK) return st;
   if (c->max_len < 1 || c->max_len > p.cfg.max_T) return DELTAKV_ERR_INVALID_ARG;
-  // the kernels count 16-row units of all pairs, and 1024-row blocks of a grid, in 32 bits
+  // the kernels count 16-row units of all pairs, and 1024-row blocks of a grid, in 32 bits; a warp's look ahead
+  // reaches up to two batches of eight by 32 units past the last
+  constexpr int64_t kMostUnits = INT32_MAX - 1024;
   if ((int64_t)p.cfg.batch * p.cfg.kv_heads > (INT32_MAX >> 4) ||
-      (int64_t)p.cfg.batch * p.cfg.kv_heads * ceil_div64(c->max_len, 16) > INT32_MAX)
+      (int64_t)p.cfg.batch * p.cfg.kv_heads * ceil_div64(c->max_len, 16) > kMostUnits)
     return DELTAKV_ERR_UNSUPPORTED;
   if (c->max_pages < ceil_div64(c->max_len, c->tokens_per_page)) return DELTAKV_ERR_INVALID_ARG;
   if (!aligned(c->pool, 16) || !aligned(workspace, 16) || !aligned(c->page_table, 4) || !aligned(c->lens, 4))

@@ -370,7 +370,7 @@ typedef struct {
  * time: calls that can run at once (on several streams, in graphs replayed on
  * several) take a workspace each, and none of them may write what another
  * reads.
- * UNSUPPORTED: B H ceil(max_len / 16) of 2^31 and more. */
+ * UNSUPPORTED: B H ceil(max_len / 16) of 2^31 - 1024 and more. */
 typedef struct {
     void* pool;                 /* device, 16-byte aligned, pool_bytes */
     int32_t n_pages;

@@ -261,3 +261,15 @@ def test_a_cache_passes_the_tensors_it_shows(lib):
     more.set_(torch.ones(2, dtype=torch.int32))
     with pytest.raises(ValueError):
         cache._view(10)
+
+
+@pytest.mark.parametrize("batch,max_len", [(2**27 - 1, 256), (2**27 - 64, 256), (2**21 - 1, 2**14)])
+def test_calls_refuse_more_rows_than_their_unit_counts_hold(lib, batch, max_len):
+    """A little below 2^31 units of 16 rows the look ahead past the last unit
+    would wrap round: refused before any launch."""
+    p = _plan(batch=batch, kv_heads=1, q_heads=1, max_T=max_len, dtype=dkv.F32)
+    view = _view(max_len=max_len, max_pages=max_len // 64)
+    got = _calls(lib, p.handle, view)[:2]
+    got.append(lib.deltakv_kv_evict(p.handle, ctypes.byref(view), FAKE, 0, 0, FAKE, FAKE, FAKE, FAKE, max_len, FAKE,
+                                    FAKE, 1 << 40, None))
+    assert got == [UNSUPPORTED] * 3
