@@ -38,6 +38,13 @@ namespace {
 
 bool aligned(const void* ptr, uintptr_t n) { return ((uintptr_t)ptr & (n - 1)) == 0; }
 
+// Rows of d elements at b * sb + h * sh share none: one stride steps over all rows of the other.  (A stride of a
+// dimension of one counts for nothing.)
+bool rows_apart(int64_t B, int64_t H, int64_t sb, int64_t sh, int64_t d) {
+  if (B == 1 || H == 1) return (B == 1 || sb >= d) && (H == 1 || sh >= d);
+  return (sh >= d && (sb - d) / sh >= H - 1) || (sb >= d && (sh - d) / sb >= B - 1);
+}
+
 deltakv_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DELTAKV_OK : DELTAKV_ERR_CUDA; }
 
 // log2 of a page's rows, or -1 where the size is not built
@@ -149,6 +156,8 @@ deltakv_status deltakv_kv_decode_attention(deltakv_plan_t plan, const deltakv_kv
   if ((q_strides[0] * p.esize) % 16 || (q_strides[1] * p.esize) % 16 || (out_strides[0] * 4) % 16 ||
       (out_strides[1] * 4) % 16)
     return DELTAKV_ERR_ALIGNMENT;
+  if (!rows_apart(p.cfg.batch, p.cfg.q_heads, out_strides[0], out_strides[1], p.cfg.d_h))
+    return DELTAKV_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(weights, 16)) return DELTAKV_ERR_ALIGNMENT;
   return from_cuda(launch_kv_attend(p, v, q, q_strides[0], q_strides[1], out, out_strides[0], out_strides[1], lse,
                                     weights, cap, decay, workspace, (cudaStream_t)stream));

@@ -425,7 +425,9 @@ deltakv_status deltakv_kv_append(deltakv_plan_t plan, const deltakv_kv_cache* ca
  * for the same rows, the accumulated attention weight deltakv_kv_evict ranks
  * by.  Rows are split over the whole GPU whatever their lengths and joined by
  * their log-sum-exp; the result does not depend on timing.
- *   q, out     : as for deltakv_decode_attention
+ *   q, out     : as for deltakv_decode_attention; one of out's strides steps
+ *                over all rows of the other (INVALID_ARG where rows could
+ *                share elements; q's may, as in a broadcast one)
  *   lse        : device float32 [B][Hq] or NULL: log sum_r exp(logit_r)
  *   weights    : device float32 [B][H][cap] or NULL; cap >= max_len
  *   decay      : >= 0 and finite (1: plain sums); ignored without weights

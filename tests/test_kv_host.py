@@ -273,3 +273,24 @@ def test_calls_refuse_more_rows_than_their_unit_counts_hold(lib, batch, max_len)
     got.append(lib.deltakv_kv_evict(p.handle, ctypes.byref(view), FAKE, 0, 0, FAKE, FAKE, FAKE, FAKE, max_len, FAKE,
                                     FAKE, 1 << 40, None))
     assert got == [UNSUPPORTED] * 3
+
+
+@pytest.mark.parametrize("B,Hq,strides,code", [
+    (2, 8, (0, 128), INVALID), (2, 8, (1024, 0), INVALID), (2, 8, (0, 0), INVALID), (2, 8, (128, 128), INVALID),
+    (2, 8, (1020, 128), INVALID), (2, 8, (1024, 124), INVALID), (2, 8, (64, 1024), INVALID),
+    (2, 8, (128, 252), INVALID), (1, 8, (0, 124), INVALID), (2, 1, (124, 0), INVALID),
+    (2, 8, (2**60, 2**60), INVALID),
+    # apart: the call goes on to its unaligned query
+    (2, 8, (1024, 128), ALIGNMENT), (2, 8, (2**60, 128), ALIGNMENT), (2, 8, (128, 256), ALIGNMENT),
+    (2, 8, (128, 2**60), ALIGNMENT), (1, 8, (0, 128), ALIGNMENT), (1, 8, (2**60, 132), ALIGNMENT),
+    (2, 1, (128, 0), ALIGNMENT), (1, 1, (0, 0), ALIGNMENT),
+])
+def test_decode_refuses_outputs_that_overlap(lib, B, Hq, strides, code):
+    """Rows of out that share elements would be written by several heads at
+    once; a broadcast q is read, and stays allowed."""
+    p = _plan(batch=B, kv_heads=1, q_heads=Hq)
+    two = ctypes.c_int64 * 2
+    assert lib.deltakv_kv_decode_attention(p.handle, ctypes.byref(_view()), FAKE + 2, two(0, 0), FAKE, two(*strides),
+                                           None, None, 0, 1.0, FAKE, 1 << 40, None) == code
+    rows = sorted(b * strides[0] + h * strides[1] for b in range(B) for h in range(Hq))
+    assert (code == ALIGNMENT) == all(y - x >= 128 for x, y in zip(rows, rows[1:]))
