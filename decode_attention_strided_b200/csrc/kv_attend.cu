@@ -439,6 +439,7 @@ __device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0
 template <int DH, int GP_>
 struct Bf16Rows {
   using E = __nv_bfloat16;
+  static constexpr bool kSplit = true;     // weights in terms: finish() may refuse
   static constexpr int GP = GP_;           // 2, 4 or 8: heads per copy of them in the columns
   static constexpr int kTerms = GP == 8 ? 3 : GP == 4 ? 2 : 1;  // products per group
   static constexpr int kG = kUnitRows<E, DH> / kGroup;
@@ -679,6 +680,7 @@ struct Bf16Rows {
 template <int DH, int GP_>
 struct F32Rows {
   using E = float;
+  static constexpr bool kSplit = false;    // weights as they are: every result is the formula's
   static constexpr int GP = GP_;
   static constexpr int kRows = kUnitRows<float, DH>;
   static constexpr int kL = DH * GP / 64 < 4 ? 4 : DH * GP / 64;  // 4, 8 or 16
@@ -845,7 +847,7 @@ struct F32Rows {
     }
   }
 
-  __device__ __forceinline__ bool finish(Merge<DH, GP>& mg, int buf, int warp, int lane) {
+  __device__ __forceinline__ void finish(Merge<DH, GP>& mg, int buf, int warp, int lane) {
 #pragma unroll
     for (int s = kL; s < 32; s <<= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
     const int head = head_of(lane);
@@ -861,11 +863,10 @@ struct F32Rows {
       }
       if (lane < kV) *reinterpret_cast<float4*>(&mg.o[buf][warp][g][lane * 4]) = o[g];
     }
-    return true;
   }
 };
 
-// A warp's units u, u + kWarps, .. < ue of a pair (at), computed row by row in
+// A warp's units u, u + kWarps, .. < ue of a bfloat16 pair (at), computed row by row in
 // float32 from global memory, for sums that an infinity or a NaN among the rows
 // made worthless: every product is then one of a weight and a value, as in the
 // formula.
@@ -903,6 +904,17 @@ __device__ __noinline__ void plain_rows(const AttendArgs& a, Merge<DH, GP>& mg, 
       mg.l[buf][warp][g] = l;
     }
     for (int i = 0; i < kN; ++i) mg.o[buf][warp][g][i * 32 + lane] = o[i];
+  }
+}
+
+// Leave a warp's result for its units u, u + kWarps, .. < ue of a pair (at).
+template <int DH, typename Rows>
+__device__ __forceinline__ void leave_result(const AttendArgs& a, Rows& rows, Merge<DH, Rows::GP>& mg, int buf, Place at,
+                                             int u, int ue, int warp, int lane) {
+  if constexpr (Rows::kSplit) {
+    if (!rows.finish(mg, buf, warp, lane)) plain_rows(a, mg, buf, at, u, ue, warp, lane);
+  } else {
+    rows.finish(mg, buf, warp, lane);
   }
 }
 
@@ -958,8 +970,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
       float* xl = a.w ? a.dots + ((int64_t)at.bh * a.c.max_len + r) * a.G : nullptr;
       rows.step(a, in, min(at.len - r, kRows), xl, lane);
     }
-    if (!rows.finish(sm.merge, held, warp, lane))
-      plain_rows(a, sm.merge, held, at, u + ((u_first + warp - u) & (kWarps - 1)), ue, warp, lane);
+    leave_result<DH>(a, rows, sm.merge, held, at, u + ((u_first + warp - u) & (kWarps - 1)), ue, warp, lane);
     if (threadIdx.x == 0) {
       sm.merge.bh[held] = at.bh;
       sm.merge.slot[held] = u == at.s && ue == at.s + ub ? -1 : u == u_first ? 0 : 1;
@@ -1020,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_short_kernel(const __gr
     float* xl = a.w ? a.dots + ((int64_t)bh * a.c.max_len + r) * a.G : nullptr;
     rows.step(a, in, min(len - r, kRows), xl, lane);
   }
-  if (!rows.finish(sm.merge, 0, warp, lane)) plain_rows(a, sm.merge, 0, at, u0 + warp, u1, warp, lane);
+  leave_result<DH>(a, rows, sm.merge, 0, at, u0 + warp, u1, warp, lane);
   in.drain();
   __syncthreads();
   // this CTA's part, where the rows were: o[G][DH], m[kMaxG], l[kMaxG]

@@ -226,11 +226,12 @@ __device__ __forceinline__ int scan_counts(SelSmem& sm) {
 }
 
 // kPer: rows per thread in registers; kWords: words of a row for the clusters
-// to make the moves themselves, or 0.
+// to make the moves themselves, with every run in registers, or 0.
 template <int kPer, int kWords>
 __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_constant__ EvictArgs a) {
   namespace cg = cooperative_groups;
   constexpr int kChunk = kPer * kSelThreads;
+  constexpr bool kOne = kWords > 0;  // (a run of more rows than the registers hold is never launched so)
   __shared__ SelSmem sm;
   const cg::cluster_group cl = cg::this_cluster();
   const int C = a.cluster, rank = C == 1 ? 0 : (int)cl.block_rank();
@@ -254,7 +255,8 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
   };
   auto peer = [&](auto* p, int c) { return C == 1 ? p : cl.map_shared_rank(p, c); };
   // ---- keys and positions of rows r0 + j kSelThreads + tid, their range, the largest position, and the pages
-  const bool resident = run <= kChunk;
+  const bool resident = kOne || run <= kChunk;
+  auto next = [&](int r0) { return kOne ? hi : r0 + kChunk; };
   uint32_t key[kPer];
   int ps[kPer];
   auto load = [&](int r0) {
@@ -276,7 +278,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
   };
   uint32_t kmin = 0xffffffffu, kmax = 0u;
   int last = INT32_MIN, bad = 0;
-  for (int r0 = lo; r0 < hi; r0 += kChunk) {
+  for (int r0 = lo; r0 < hi; r0 = next(r0)) {
     load(r0);
     const int in = hi - r0 - tid;
 #pragma unroll
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
     for (int i = 0; i < kFew; ++i) {
       if (i >= n - m) break;
       uint64_t least = ~0ull;
-      for (int r0 = lo; r0 < hi; r0 += kChunk) {
+      for (int r0 = lo; r0 < hi; r0 = next(r0)) {
         fetch(r0);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
       int* hist = sm.hist[buf];
       for (int i = tid; i <= kBins; i += kSelThreads) hist[i] = 0;
       __syncthreads();
-      for (int r0 = lo; r0 < hi; r0 += kChunk) {
+      for (int r0 = lo; r0 < hi; r0 = next(r0)) {
         fetch(r0);
         const int in = hi - r0 - tid;
         int guarded = 0;
@@ -481,7 +483,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
     uint32_t hm = 0, mm = 0;  // bit j: the thread's j-th row of the last chunk counted is a hole (mover)
     for (int pass = 0; pass < 2; ++pass) {
       int eq_at = eq_before, holes = hole_at, movers = move_at;
-      for (int r0 = lo; r0 < hi; r0 += kChunk) {
+      for (int r0 = lo; r0 < hi; r0 = next(r0)) {
         int all = 0;
         if (pass == 0 || !resident) {  // (of a single chunk, the first pass has it all)
           fetch(r0);
