@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 
 import torch
@@ -397,7 +398,10 @@ def alloc_kv_workspace(p: Plan, max_len: int, weights: bool = False, device="cud
                        device=device)
 
 
-_I2, _I3 = ctypes.c_int64 * 2, ctypes.c_int64 * 3
+@functools.lru_cache(maxsize=256)
+def _strides(*n):
+    """A C array of strides, which the calls only read."""
+    return (ctypes.c_int64 * len(n))(*n)
 
 
 def _kv_tensor(name, t, dtype, shape, dev):
@@ -548,8 +552,8 @@ def kv_append(p: Plan, cache: KVCache, max_len: int, K, V, workspace, n_tokens=N
         raise ValueError(f"weights and pos must have the same cap, got {cap} and {cap_p}")
     view, ws, nbytes, st = cache._call("deltakv_kv_append", p, max_len, workspace, stream)
     code = _lib.deltakv_kv_append(p.handle, view, n_new, K.data_ptr(), V.data_ptr(),
-                                  _I3(ks[0] if B > 1 else 0, ks[1] if H > 1 else 0, ks[2] if n_new > 1 else d), nt, fp,
-                                  w, pp, cap_p, tw, ws, nbytes, st)
+                                  _strides(ks[0] if B > 1 else 0, ks[1] if H > 1 else 0, ks[2] if n_new > 1 else d),
+                                  nt, fp, w, pp, cap_p, tw, ws, nbytes, st)
     if code:
         _check("deltakv_kv_append", code)
 
@@ -568,8 +572,8 @@ def kv_decode_attention(p: Plan, cache: KVCache, max_len: int, q, out, workspace
     view, ws, nbytes, st = cache._call("deltakv_kv_decode_attention", p, max_len, workspace, stream)
     many, heads = c.batch > 1, c.q_heads > 1
     code = _lib.deltakv_kv_decode_attention(
-        p.handle, view, q.data_ptr(), _I2(qs[0] if many else 0, qs[1] if heads else 0), out.data_ptr(),
-        _I2(os_[0] if many else 0, os_[1] if heads else 0), lp, w, cap, decay, ws, nbytes, st)
+        p.handle, view, q.data_ptr(), _strides(qs[0] if many else 0, qs[1] if heads else 0), out.data_ptr(),
+        _strides(os_[0] if many else 0, os_[1] if heads else 0), lp, w, cap, decay, ws, nbytes, st)
     if code:
         _check("deltakv_kv_decode_attention", code)
 
