@@ -140,3 +140,56 @@ def evict64(n, budget, n_first, n_recent, w, pos):
     src = np.arange(m)
     src[~kept[:m]] = np.arange(m, n)[kept[m:]]
     return m, src
+
+
+def few_queries(c: KvCase):
+    """Queries of two non-zero elements each, at places that differ by head:
+    logits come out almost exact, and within about one of each other, so that
+    what is left of an error is the softmax weights' and the sums'."""
+    q = torch.zeros(c.B * c.Hq, c.d)
+    i = torch.arange(c.B * c.Hq)
+    at = 7 * i + 3
+    v = 4.0 if c.d == 128 else 3.0
+    q[i, at % c.d] = v
+    q[i, (at + 1 + 5 * (i % 11)) % c.d] = -v
+    return q.view(c.B, c.Hq, c.d).to(c.torch_dtype())
+
+
+def unit_rows(c: KvCase):
+    """Rows of one step of a warp: 8 KB of K."""
+    return 8192 // (c.d * (4 if c.dtype == dkv.F32 else 2))
+
+
+def few_bounds(q, K, V, p, unit):
+    """attend_bounds for queries of few non-zero elements and pairs of at most
+    eight units of rows, counted term by term: (out, lse, relative error of a
+    weight).  u = 2^-24.
+
+    A logit: one rounding or truncation (2 u) per non-zero product.  Its
+    exponent, one fused multiply-add: u of its distance from the maximum, plus
+    3 u of that distance for the scale's roundings; the maximum's own rounding
+    is common to all rows.  2^x: 4 u.  Where the rows are several units (a warp
+    each), a part is scaled twice, by 2^x of a difference of maxima each time.
+    Additions of the sum of p V, 2 u each: a unit's rows (a product's terms
+    come smallest first; with several 16-row groups each of the three terms is
+    added to a full sum), the running sum, two for the columns of a head, the
+    warps, the parts; of the sum of p, u each, no more of them.  What three
+    bfloat16 terms leave of a weight is below u / 4; 1 / l and its product two
+    u."""
+    n, d = K.shape
+    u = 2.0 ** -24
+    units = -(-n // unit)
+    assert units <= 8
+    x = q @ K.T / math.sqrt(d)
+    span = x.max(axis=1) - x.min(axis=1)
+    mag = (np.abs(q) @ np.abs(K).T).max(axis=1) / math.sqrt(d)
+    dx = 2 * u * np.count_nonzero(q, axis=1) * mag
+    stages = 0 if units == 1 else 2
+    ep = 2 * dx + 4 * u * span + 4 * u + stages * (4 * u + 1.5 * u * span)
+    rows = min(n, unit)
+    adds = (rows if rows <= 16 else 3 * rows) + 4 + 2 * (units - 1)
+    rel = 2 * ep + 3 * u * adds + 3 * u
+    top = x.max(axis=1)
+    lse = top + np.log(np.exp(x - top[:, None]).sum(axis=1))
+    tol_lse = dx + 4 * u * np.abs(top) + ep + u * adds + 4 * u * (1 + np.abs(lse) + math.log(n))
+    return rel[:, None] * (p @ np.abs(V)), tol_lse, rel + 4 * u

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from decode_attention_strided_b200 import deltakv as dkv
-from kv_util import KvCase, Setup, attend64, attend_bounds, evict64
+from kv_util import KvCase, Setup, attend64, attend_bounds, evict64, few_bounds, few_queries, unit_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -884,3 +884,95 @@ def test_evict_in_place_leaves_a_length_out_of_range_as_it_is(n, bad):
     s.c = KvCase([[n, 100, 100]], 3, max_len=n)
     s.lens_host = torch.tensor(s.c.lens, dtype=torch.int32)
     assert _evict_check(s, [[100, 100, 100]], 0, 0, wd.cpu(), pd.cpu(), True) == 0
+
+
+# ---- every kernel that the dispatch can choose
+
+def _ran(p, call):
+    """Names of the kernels that a call launched."""
+    dkv.profile_collect(p)
+    dkv.set_profiling(p, True)
+    try:
+        got = call()
+        return got, set(dkv.profile_collect(p))
+    finally:
+        dkv.set_profiling(p, False)
+
+
+SHORT, CUT, WEIGHTS = {"kv_attend_short"}, {"kv_attend", "kv_join"}, {"kv_attend", "kv_join", "kv_weights"}
+
+
+@pytest.mark.parametrize("form", ["cluster", "cut"])
+@pytest.mark.parametrize("G", range(1, 9))
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [dkv.BF16, dkv.F32], ids=["bf16", "f32"])
+def test_attend_few_rows_closely(dtype, d, G, form):
+    """Both types and head sizes, one to eight heads a kv-head and both forms
+    of the split, with weights, on pairs of few rows and almost exact logits:
+    within bounds that a weight of two bfloat16 terms does not meet
+    (test_the_counted_bounds_tell_a_missing_weight_term)."""
+    H = 6
+    pattern = (2, 3, 2, 17, 2, 100, 2, 0, 2, 33, 1, 16)
+    c = KvCase([[pattern[(b * H + h) % 12] for h in range(H)] for b in range(8)], H * G, d=d, page=32, dtype=dtype,
+               max_len=2200 if form == "cut" else 0, seed=G)
+    s = Setup(c)
+    s.q = few_queries(c)
+    (out, lse, w), ran = _ran(s.p, lambda: _attend(s, decay=0.5))
+    assert dkv.device_status(s.p, s.ws) == 0
+    assert ran == (WEIGHTS if form == "cut" else SHORT)
+    out, lse, w = (x.cpu().double().numpy() for x in (out, lse, w))
+    w0 = s.w.double().numpy()
+    for b in range(c.B):
+        for h in range(H):
+            n, g = c.lens[b][h], slice(h * G, h * G + G)
+            if n == 0:
+                assert (out[b, g] == 0).all() and (lse[b, g] == -np.inf).all() and (w[b, h] == w0[b, h]).all()
+                continue
+            q, K, V = (x.double().numpy() for x in (s.q[b, g], s.K[b, h], s.V[b, h]))
+            ref, ref_lse, p = attend64(q, K, V)
+            tol, tol_lse, rel = few_bounds(q, K, V, p, unit_rows(c))
+            err = np.abs(out[b, g] - ref) / tol
+            assert err.max() <= 1, (b, h, n, float(err.max()))
+            err = np.abs(lse[b, g] - ref_lse) / tol_lse
+            assert err.max() <= 1, (b, h, n, float(err.max()))
+            want = 0.5 * w0[b, h, :n] + p.sum(axis=0)
+            # the heads' sum and the old weight's product: G + 1 roundings
+            err = np.abs(w[b, h, :n] - want) / (rel @ p + (G + 1) * 2.0 ** -24 * want)
+            assert err.max() <= 1, (b, h, n, float(err.max()))
+            assert (w[b, h, n:] == w0[b, h, n:]).all()
+
+
+@pytest.mark.parametrize("weights", [False, True], ids=["plain", "weights"])
+@pytest.mark.parametrize("name,case", ATTEND, ids=[n for n, _ in ATTEND])
+def test_attend_cases_take_the_form_they_name(name, case, weights):
+    cut = WEIGHTS if weights else CUT
+    _, ran = _ran((s := Setup(case)).p, lambda: _attend(s, weights))
+    # as they are: a cluster per pair up to 128 pairs, but for rows of more than 16 units a CTA ("long": 20011 rows are
+    # 626 units, "f32_g3": 5003 are 313, both for clusters of eight)
+    assert ran == (cut if name in ("long", "f32_g3", "many_pairs", "mostly_empty") else SHORT)
+    if case.B * case.H <= 32:
+        _, ran = _ran((s := Setup(dataclasses.replace(case, max_len=40000))).p, lambda: _attend(s, weights))
+        assert ran == cut
+
+
+@pytest.mark.parametrize("name,case", EVICT_FORMS, ids=[e[0] for e in EVICT_FORMS])
+def test_evict_cases_take_the_form_they_name(name, case):
+    """The clusters make the moves up to eight rows a thread, the second kernel
+    from there on."""
+    s = Setup(case)
+    w, pos = _meta(case, 5, "random", case.n)
+    budget = torch.tensor([[n // 2 for n in row] for row in case.lens], dtype=torch.int32, device="cuda")
+    _, ran = _ran(s.p, lambda: dkv.kv_evict(s.p, s.cache, case.n, budget, w.cuda(), pos.cuda(), s.ws))
+    assert dkv.device_status(s.p, s.ws) == 0
+    assert ran == ({"kv_select", "kv_move"} if name.startswith("16") else {"kv_select"})
+
+
+@pytest.mark.parametrize("kind", ["random", "equal", "few", "special"])
+@pytest.mark.parametrize("drop", ["two", "half"])
+def test_evict_short_rows_of_d64(drop, kind):
+    """Two rows a thread at most, rows of 128 bytes, moved by the block."""
+    case = KvCase([[900, 1, 33], [0, 1999, 2000]], 3, d=64, page=16)
+    s = Setup(case)
+    w, pos = _meta(case, 5, kind, case.n + 1)
+    budget = [[max(0, n - 2) if drop == "two" else n // 2 for n in row] for row in case.lens]
+    assert _evict_check(s, budget, 1, 9, w, pos, True) == 0

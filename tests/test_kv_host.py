@@ -9,7 +9,7 @@ import torch
 
 from decode_attention_strided_b200 import build as dkv_build
 from decode_attention_strided_b200 import deltakv as dkv
-from kv_util import attend64, evict64
+from kv_util import KvCase, attend64, evict64, few_bounds, few_queries, unit_rows
 
 OK, INVALID, UNSUPPORTED, ALIGNMENT, WORKSPACE = 0, 1, 2, 3, 4
 
@@ -294,3 +294,33 @@ def test_decode_refuses_outputs_that_overlap(lib, B, Hq, strides, code):
                                            None, None, 0, 1.0, FAKE, 1 << 40, None) == code
     rows = sorted(b * strides[0] + h * strides[1] for b in range(B) for h in range(Hq))
     assert (code == ALIGNMENT) == all(y - x >= 128 for x, y in zip(rows, rows[1:]))
+
+
+def _bf16(x):
+    return torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).bfloat16().float().numpy()
+
+
+@pytest.mark.parametrize("terms", [3, 2, 1])
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_counted_bounds_tell_a_missing_weight_term(terms, d):
+    """A weight of three bfloat16 terms stays inside few_bounds, one that lost
+    its third or its second does not."""
+    c = KvCase([[2] * 6] * 8, 6, d=d)
+    q = few_queries(c).double().numpy()
+    g = torch.Generator().manual_seed(11)
+    worst = 0.0
+    for b in range(c.B):
+        for h in range(c.H):
+            K, V = (torch.randn(2, d, generator=g).bfloat16().double().numpy() for _ in range(2))
+            qh = q[b, h:h + 1]
+            ref, _, p = attend64(qh, K, V)
+            x = (qh @ K.T / math.sqrt(d))[0]
+            w = np.exp(x - x.max()).astype(np.float32)
+            rest, got = w.copy(), np.zeros(d)
+            for _ in range(terms):
+                t = _bf16(rest)
+                got += t.astype(np.float64) @ V
+                rest = rest - t
+            tol, _, _ = few_bounds(qh, K, V, p, unit_rows(c))
+            worst = max(worst, float((np.abs(got / w.astype(np.float64).sum() - ref[0]) / tol[0]).max()))
+    assert worst < 0.5 if terms == 3 else worst > 1.5
