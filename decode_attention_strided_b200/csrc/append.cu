@@ -495,25 +495,6 @@ __global__ void __launch_bounds__(kFinishThreads, 1)
   if (tid < k) idx[((int64_t)bh * P.n_code_cap + row) * k + tid] = tid < k_eff ? sel[tid] : -1;
 }
 
-// Launch with programmatic stream serialisation: the grid may start while
-// the previous kernel on the stream is still running, and waits for it in
-// grid_dep_wait().
-template <typename... KArgs, typename... Args>
-static cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                              Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 template <typename E, int NV>
 static cudaError_t launch_rows(const AppendParams& P, int per, int nsplit, dim3 gs, dim3 gf, const KVView& kv,
                                const void* W1, const float* b1, const void* W2, const float* b2, const E* refk,

@@ -14,14 +14,13 @@ namespace dkv {
 // work ahead of it on the stream still runs, and waits for that work itself
 // (griddepcontrol.wait) before it reads or writes anything another grid does.
 template <typename... P, typename... A>
-cudaError_t launch_pdl(void (*kern)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st,
-                       const A&... args) {
+cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, dim3 threads, size_t smem, cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
+  cfg.gridDim = grid;
+  cfg.blockDim = threads;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = &attr;
