@@ -35,13 +35,15 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kGroup = 16;         // rows of the smallest page
 constexpr int kSlotBytes = 8192;   // K or V rows of one unit of the split
 constexpr int kSlots = 2;          // of a warp's ring: K rows, V rows
-constexpr int kMinUnits = 4;       // a CTA gets at least these, or fewer CTAs work
+constexpr int kMinUnits = 4;       // below a full grid a CTA gets these at most, and so many CTAs work (5 units: 3 and 2)
 // A cluster per pair instead of the cut (one kernel instead of two): where its
 // CTAs find room at once (16 clusters of eight did not, 32 of four did) and take
 // 16 units at most.  bf16, d_h 128, four heads, us replayed, cluster / cut: 8
 // pairs of 513 rows 8.2 / 10.3, of 4096 (16 units a CTA) 12.3 / 14.4, of 8192
 // 18.6 / 18.4; 64 pairs of 1024 14.4 / 16.3; one pair of 8192 18.4 / 13.2.  Lengths
-// that differ cost the cluster more, the cut nothing, hence no more units.
+// that differ cost the cluster more, the cut nothing, hence no more units.  Measured
+// without weights, with which the cut is three kernels instead of two; the limits hold
+// for every type, head size and head count and with weights, where they were not.
 constexpr int kShortUnits = 16;
 constexpr int short_ctas(int cluster) { return cluster == 8 ? 96 : 128; }
 // rows per unit
@@ -260,7 +262,7 @@ __device__ __forceinline__ float ex2(float x) {
 // ---- the rows' way into shared memory
 // A warp takes every eighth unit of its CTA's range through a slot for K rows
 // and one for V rows of its own: lane 0 issues bulk copies (one per slot where
-// a page holds a unit, else one per page), a barrier per slot tells when they
+// a page holds a unit, else a lane per 16 rows its own), a barrier per slot tells when they
 // have landed, and a slot is refilled as soon as its rows are in registers.  No
 // other warp takes part, so the warps drift freely between the segments' ends.
 // Plain copies in this pattern reach 7.3 TB/s with 8 KB copies and 96 to 128 KB

@@ -447,7 +447,8 @@ class KVCache:
     max_pages], lens int32 [B, H] (valid rows).  Holds the tensors; the caller
     may change their contents between calls, and may assign another pool,
     page_table or lens, which is checked like the first one and used from the
-    next call on (a graph keeps the tensors that it was captured with)."""
+    next call on (a captured call goes on using those that it was captured
+    with)."""
 
     def __init__(self, p: Plan, pool, page_table, lens):
         self._bind(p, pool, page_table, lens)

@@ -343,9 +343,11 @@ deltakv_status deltakv_decode_attention_paged(deltakv_plan_t plan, const int32_t
                                               deltakv_stream_t stream);
 
 /* ---- Plain paged cache: K and V rows as they are, in pages of a shared pool.
- * What a model holds before (or beside) compression: layers or recent tokens
- * kept whole, the full cache a compressed one is compared with, and caches
- * made smaller by dropping tokens.  A page is tokens_per_page consecutive rows
+ * What a model holds before (or beside) compression: layers kept whole, the
+ * full cache a compressed one is compared with, and caches made smaller by
+ * dropping tokens.  (A sequence whose recent tokens are plain and whose others
+ * are compressed is not covered: joining the two outputs takes the log-sum-exp
+ * of both, and the compressed decode calls return none.)  A page is tokens_per_page consecutive rows
  * of one (sequence, kv-head); lengths are per (sequence, kv-head).
  *
  * Pool layout: the K plane, then the V plane, each [n_pages][tokens_per_page]
@@ -449,8 +451,8 @@ deltakv_status deltakv_kv_decode_attention(deltakv_plan_t plan, const deltakv_kv
  * below m stay where they are; kept rows at or past m move, in order, into the
  * dropped rows below m, so that rows 0 .. m-1 are the kept ones and only what
  * has to move moves (attention does not depend on the rows' order; pos says
- * which token a row is).  K and V rows move in place.  Pages past ceil(m / tokens_per_page) are
- * free afterwards.
+ * which token a row is).  K and V rows move in place.  Pages past
+ * ceil(m / tokens_per_page) are free afterwards.
  *   budget     : device int32 [B][H]; a negative entry drops nothing and is
  *                reported as DEVICE_BOUNDS
  *   n_first, n_recent : >= 0, their sum <= max_T
@@ -474,9 +476,9 @@ deltakv_status deltakv_device_status(deltakv_plan_t plan, void* workspace,
                                      deltakv_stream_t stream);
 
 /* Tracing: every call that launches kernels (compress, append, the decode
- * calls, pages_from_cache, reconstruct, the kv calls) opens an NVTX range named after the
- * call for its duration, so a tool that records NVTX ranges shows each
- * call's kernels under its name.  Without such a tool the ranges cost a
+ * calls, pages_from_cache, reconstruct, the kv calls) opens an NVTX range
+ * named after the call for its duration, so a tool that records NVTX ranges
+ * shows each call's kernels under its name.  Without such a tool the ranges cost a
  * pointer test each.
  *
  * Benchmark support: per-kernel device time.  While profiling is on for a
